@@ -8,6 +8,7 @@ load, :func:`lib` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -22,6 +23,7 @@ ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_SHAPE, ERR_WORKSPACE = 1, 2, 3, 4
 ERR_CUDA, ERR_NONFINITE, ERR_TIMEOUT, ERR_UNSUPPORTED, ERR_FORMAT = 5, 6, 7, 8, 9
 F32, BF16 = 0, 1
 FLAG_NONFINITE, FLAG_TIMEOUT, FLAG_BAD_INDEX = 1, 2, 4
+E4M3, E5M2 = 0, 1
 LINEAR_GELU_TANH = 1
 LINEAR_OUT_F32 = 2
 LINEAR_FAKE_QUANT_OUT = 4
@@ -63,6 +65,17 @@ SIGNATURES = {
     "hif4_to_e4m3": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P]),
     "hif4_gemm_f8": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _U32, _P,
                                     _P]),
+    "hif4_quantize_f8": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, _I32, _P, _I64, _P, _I64,
+                                        _P, _I64, _P, _I64, _P, _P]),
+    "hif4_gemm_f8_block": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I64, _P, ctypes.c_int, _I64, _I64,
+                                          _P, _I64, _I32, _P, _P, _I64, _U32, _P, _P]),
+    "hif4_layer_norm": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, ctypes.c_float, _P,
+                                       ctypes.c_int, _I64, _P, _P, _P]),
+    "hif4_layer_norm_f8": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, ctypes.c_float,
+                                          ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "hif4_layer_norm_backward_workspace": (_SZ, [_I64, _I64]),
+    "hif4_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P,
+                                                ctypes.c_int, _P, _I64, _P, _P, _P, _SZ, _P]),
     "hif4_debug_wait_test": (None, [ctypes.c_uint32, ctypes.c_uint64]),
     "hif4_get_status": (ctypes.c_int, [_P, _P]),
     "hif4_reset_status": (ctypes.c_int, [_P, _P]),
@@ -443,6 +456,233 @@ def ptq_state_unpack(record: bytes, device=None):
         idx = None if idx is None else idx.to(device)
         wm = None if wm is None else wm.to(device)
     return codes, meta, idx, wm
+
+
+# ------------------------------------------------- block-scaled FP8, layer norm
+
+_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+_F8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+
+
+def _cdiv(n, m):
+    return -(-n // m)
+
+
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _matrix(t, name, dtypes, shape=None):
+    """Checks a 2-D CUDA tensor whose rows are contiguous."""
+    _dev(t, name)
+    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "%s must be 2-D with contiguous rows" % name)
+    _need(t.dtype in dtypes, "%s has dtype %s" % (name, t.dtype))
+    _need(shape is None or tuple(t.shape) == tuple(shape), "%s must be %s, is %s" % (name, shape, tuple(t.shape)))
+    return t
+
+
+def _vector(t, name, dtypes, n):
+    if t is not None:
+        _dev(t, name)
+        _need(t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1),
+              "%s must be a contiguous vector of %d elements" % (name, n))
+        _need(t.dtype in dtypes, "%s has dtype %s" % (name, t.dtype))
+    return t
+
+
+def _ld(t, multiple):
+    """Leading dimension; that of a single row, which no address depends on, is rounded up."""
+    return t.stride(0) if t.shape[0] > 1 else _cdiv(t.shape[1], multiple) * multiple
+
+
+def _padded(rows, cols, dtype, multiple, device):
+    """rows x cols whose leading dimension is a multiple of `multiple` elements."""
+    return torch.empty(rows, _cdiv(cols, multiple) * multiple, dtype=dtype, device=device)[:, :cols]
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield stream
+
+
+def _place(stream, *tensors):
+    """Context of a call: its tensors' device current, `stream` (default: that
+    device's current stream) current, so that what the call allocates belongs
+    to the stream it runs on.  Yields the stream."""
+    dev = tensors[0].device
+    for t in tensors:
+        _need(t is None or t.device == dev, "tensors of one call must be on one device")
+    _need(stream is None or stream.device == dev, "the stream is on another device than the tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+        if dev.index == torch.cuda.current_device():
+            return contextlib.nullcontext(stream)
+    return _switched(dev, stream)
+
+
+def quantize_f8(x: torch.Tensor, fmt=torch.float8_e4m3fn, *, block_rows: int = 1, layout: str = "rows", out=None,
+                status=None, stream=None):
+    """FP8 codes with one FP32 scale per block of 128 (see hif4.h).
+
+    layout "rows": (q [rows, cols], scale); "cols": (qt [cols, rows], scale_t);
+    "both": (q, scale, qt, scale_t) from one read of x.  scale is
+    [ceil(cols/128), rows] for block_rows 1 and [ceil(rows/128),
+    ceil(cols/128)] for 128; scale_t likewise for the transposed matrix.
+    `out` is a tuple of those tensors to write into."""
+    _matrix(x, "x", _DTYPE)
+    _need(fmt in _F8, "fmt must be torch.float8_e4m3fn or torch.float8_e5m2")
+    _need(block_rows in (1, 128), "block_rows must be 1 or 128")
+    _need(layout in ("rows", "cols", "both"), "layout must be rows, cols or both")
+    rows, cols = x.shape
+    want = {"rows": (1,), "cols": (0,), "both": (1, 0)}[layout]
+    sizes = []
+    for direct in want:
+        r, c = (rows, cols) if direct else (cols, rows)
+        sizes += [(r, c), (_cdiv(c, 128), r) if block_rows == 1 else (_cdiv(r, 128), _cdiv(c, 128))]
+    given = tuple(out) if out is not None else ()
+    with _place(stream, x, status, *given) as s:
+        if out is None:
+            out = tuple(_padded(r, c, torch.float32 if i & 1 else fmt, 4 if i & 1 else 16, x.device)
+                        for i, (r, c) in enumerate(sizes))
+        _need(len(out) == len(sizes), "out must hold %d tensors" % len(sizes))
+        for i, (t, size) in enumerate(zip(out, sizes)):
+            _matrix(t, "out[%d]" % i, (torch.float32,) if i & 1 else (fmt,), size)
+        q, sc = (out[0], out[1]) if want[0] else (None, None)
+        qt, sct = (out[-2], out[-1]) if not want[-1] else (None, None)
+        _check("hif4_quantize_f8", lib().hif4_quantize_f8(
+            _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 16), _F8[fmt], block_rows, _ptr(q),
+            0 if q is None else _ld(q, 16), _ptr(sc), 0 if sc is None else _ld(sc, 4), _ptr(qt),
+            0 if qt is None else _ld(qt, 16), _ptr(sct), 0 if sct is None else _ld(sct, 4), _ptr(status),
+            ctypes.c_void_p(s.cuda_stream)))
+    return out
+
+
+def gemm_f8_block(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                  bias: torch.Tensor | None = None, *, b_block_rows: int = 128, out=None, out_f32: bool = False,
+                  status=None, stream=None):
+    """y = (a, sa) · (b, sb)ᵀ + bias for FP8 operands with a scale per block of
+    128 along K: a [M, K] with 1 x 128 blocks, b [N, K] with 128 x 128 blocks
+    (b_block_rows 128) or 1 x 128 blocks (1), as quantize_f8 leaves them."""
+    _matrix(a, "a", _F8)
+    M, K = a.shape
+    _matrix(b, "b", _F8)
+    N = b.shape[0]
+    _need(b.shape[1] == K, "a and b must have the same number of columns")
+    _need(b_block_rows in (1, 128), "b_block_rows must be 1 or 128")
+    units = _cdiv(K, 128)
+    _matrix(sa, "sa", (torch.float32,), (units, M))
+    _matrix(sb, "sb", (torch.float32,), (units, N) if b_block_rows == 1 else (_cdiv(N, 128), units))
+    _vector(bias, "bias", (torch.bfloat16,), N)
+    with _place(stream, a, sa, b, sb, bias, out, status) as s:
+        if out is None:
+            out = (_padded(M, N, torch.float32, 4, a.device) if out_f32 else
+                   _padded(M, N, torch.bfloat16, 8, a.device))
+        _matrix(out, "out", _DTYPE, (M, N))
+        flags = LINEAR_OUT_F32 if out.dtype == torch.float32 else 0
+        _check("hif4_gemm_f8_block", lib().hif4_gemm_f8_block(
+            _ptr(a), _F8[a.dtype], M, K, _ld(a, 16), _ptr(sa), _ld(sa, 4), _ptr(b), _F8[b.dtype], N, _ld(b, 16),
+            _ptr(sb), _ld(sb, 4), b_block_rows, _ptr(bias), _ptr(out), _ld(out, 8), flags, _ptr(status),
+            ctypes.c_void_p(s.cuda_stream)))
+    return out
+
+
+def _norm_params(gamma, beta, cols):
+    _vector(gamma, "gamma", _DTYPE, cols)
+    _vector(beta, "beta", _DTYPE, cols)
+    given = [p for p in (gamma, beta) if p is not None]
+    _need(len({p.dtype for p in given}) <= 1, "gamma and beta must have the same dtype")
+    return _DTYPE[given[0].dtype] if given else F32
+
+
+def _norm_stats(rows, save_stats, device):
+    if not save_stats:
+        return None, None
+    return (torch.empty(rows, dtype=torch.float32, device=device),
+            torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+               eps: float = 1e-6, *, out=None, out_dtype=None, save_stats: bool = False, stream=None):
+    """Layer norm of the rows of x -> y, or (y, mean, rstd) with save_stats;
+    y has out_dtype (default: x's)."""
+    _matrix(x, "x", _DTYPE)
+    rows, cols = x.shape
+    pdt = _norm_params(gamma, beta, cols)
+    with _place(stream, x, gamma, beta, out) as s:
+        if out is None:
+            dt = out_dtype if out_dtype is not None else x.dtype
+            _need(dt in _DTYPE, "out_dtype must be float32 or bfloat16")
+            out = _padded(rows, cols, dt, 8, x.device)
+        _matrix(out, "out", _DTYPE, (rows, cols))
+        mean, rstd = _norm_stats(rows, save_stats, x.device)
+        _check("hif4_layer_norm", lib().hif4_layer_norm(
+            _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 8), _ptr(gamma), _ptr(beta), pdt, float(eps), _ptr(out),
+            _DTYPE[out.dtype], _ld(out, 8), _ptr(mean), _ptr(rstd), ctypes.c_void_p(s.cuda_stream)))
+    return (out, mean, rstd) if save_stats else out
+
+
+def layer_norm_f8(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                  eps: float = 1e-6, fmt=torch.float8_e4m3fn, *, out=None, save_stats: bool = False, status=None,
+                  stream=None):
+    """layer_norm in FP32 followed by quantize_f8 in 1 x 128 blocks, in one
+    pass -> (q, scale), or (q, scale, mean, rstd) with save_stats."""
+    _matrix(x, "x", _DTYPE)
+    _need(fmt in _F8, "fmt must be torch.float8_e4m3fn or torch.float8_e5m2")
+    rows, cols = x.shape
+    pdt = _norm_params(gamma, beta, cols)
+    given = tuple(out) if out is not None else ()
+    with _place(stream, x, gamma, beta, status, *given) as s:
+        if out is None:
+            out = (_padded(rows, cols, fmt, 16, x.device),
+                   _padded(_cdiv(cols, 128), rows, torch.float32, 4, x.device))
+        q, sc = out
+        _matrix(q, "out[0]", (fmt,), (rows, cols))
+        _matrix(sc, "out[1]", (torch.float32,), (_cdiv(cols, 128), rows))
+        mean, rstd = _norm_stats(rows, save_stats, x.device)
+        _check("hif4_layer_norm_f8", lib().hif4_layer_norm_f8(
+            _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 8), _ptr(gamma), _ptr(beta), pdt, float(eps), _F8[fmt],
+            _ptr(q), _ld(q, 16), _ptr(sc), _ld(sc, 4), _ptr(mean), _ptr(rstd), _ptr(status),
+            ctypes.c_void_p(s.cuda_stream)))
+    return (q, sc, mean, rstd) if save_stats else (q, sc)
+
+
+def layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    return int(lib().hif4_layer_norm_backward_workspace(rows, cols))
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        gamma: torch.Tensor | None = None, *, out=None, workspace=None, stream=None):
+    """Gradients of layer_norm -> (dx, dgamma, dbeta), from the statistics it
+    saved.  dx has x's dtype, dgamma and dbeta are FP32.  `out` is a tuple of
+    the three, None in the place of one that is not wanted."""
+    _matrix(x, "x", _DTYPE)
+    rows, cols = x.shape
+    _matrix(dy, "dy", (x.dtype,), (rows, cols))
+    _vector(mean, "mean", (torch.float32,), rows)
+    _vector(rstd, "rstd", (torch.float32,), rows)
+    _need(mean is not None and rstd is not None, "mean and rstd are needed")
+    pdt = _norm_params(gamma, None, cols)
+    given = tuple(out) if out is not None else ()
+    with _place(stream, x, dy, mean, rstd, gamma, workspace, *given) as s:
+        if out is None:
+            out = (_padded(rows, cols, x.dtype, 8, x.device),
+                   torch.empty(cols, dtype=torch.float32, device=x.device),
+                   torch.empty(cols, dtype=torch.float32, device=x.device))
+        dx, dgamma, dbeta = out
+        if dx is not None:
+            _matrix(dx, "out[0]", (x.dtype,), (rows, cols))
+        _vector(dgamma, "out[1]", (torch.float32,), cols)
+        _vector(dbeta, "out[2]", (torch.float32,), cols)
+        if workspace is None:
+            need = layer_norm_backward_workspace(rows, cols)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        _check("hif4_layer_norm_backward", lib().hif4_layer_norm_backward(
+            _ptr(dy), _ld(dy, 8), _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 8), _ptr(mean), _ptr(rstd),
+            _ptr(gamma), pdt, _ptr(dx), 0 if dx is None else _ld(dx, 8), _ptr(dgamma), _ptr(dbeta),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream)))
+    return dx, dgamma, dbeta
 
 
 def get_status(status: torch.Tensor, stream=None) -> int:

@@ -238,5 +238,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N)
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// The same with E4M3 (format code 0) or E5M2 (1) chosen for each operand.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(uint32_t M, uint32_t N, bool a_e5m2, bool b_e5m2)
+{
+    return idesc_e4m3_f32(M, N) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10);
+}
+
 } // namespace sm100
 } // namespace hif4

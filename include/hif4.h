@@ -63,6 +63,10 @@ typedef enum {
 
 typedef enum { HIF4_F32 = 0, HIF4_BF16 = 1 } hif4_dtype;
 
+/* FP8 formats of the block-scaled calls: E4M3 (largest finite value 448) and
+ * E5M2 (57344), round to nearest even, saturating. */
+typedef enum { HIF4_E4M3 = 0, HIF4_E5M2 = 1 } hif4_f8_format;
+
 /* Bits of the device status word. */
 #define HIF4_FLAG_NONFINITE 0x1u /* NaN -> 0, +-Inf -> +-FLT_MAX was applied */
 #define HIF4_FLAG_TIMEOUT 0x2u   /* a pipeline wait hit its iteration limit */
@@ -236,6 +240,121 @@ hif4_status hif4_to_e4m3(const uint8_t *codes, const uint32_t *meta, int64_t row
 hif4_status hif4_gemm_f8(const uint8_t *a, int64_t M, int64_t K, int64_t lda, const float *sa, int64_t lds_a,
                          const uint8_t *b, int64_t N, int64_t ldb, const float *sb, int64_t lds_b, void *y,
                          int64_t ldy, uint32_t flags, uint32_t *status, hif4_stream_t stream);
+
+/*
+ * Block-scaled FP8 linears and the layer norm in front of them.  The linears
+ * that the W4A4 policy keeps out of HiF4 [TA summary, "Method overview":
+ * boundary modules stay in higher precision] can run in FP8 with one FP32
+ * scale per block of 128 elements; the source pages describe no such calls,
+ * so their definitions are the library's own.
+ *
+ * Layouts.  Code matrices are row-major bytes, 16-byte aligned, leading
+ * dimensions multiples of 16.  Scales of 1 x 128 blocks are block-major:
+ * scale[u * lds + r] belongs to columns 128 u .. 128 u + 127 of row r.
+ * Scales of 128 x 128 blocks: scale[(r / 128) * lds + c / 128].  Any sizes:
+ * the last block of a row or column is shorter.
+ *
+ * hif4_quantize_f8 — per block, with a = max(max|x|, 2^-100) and F the
+ * format's largest finite value:
+ *   scale = fl32(a / F),  r = fl32(F / a),  q = RNE_f8(fl32(x r)), saturating;
+ *   NaN -> 0 and +-Inf -> +-FLT_MAX first (sets HIF4_FLAG_NONFINITE).
+ * x          rows x cols, F32 or BF16, ldx.
+ * block_rows 1: q, scale are x's codes in 1 x 128 blocks along its rows, and
+ *            qt, scale_t those of the transposed matrix (cols x rows) in
+ *            1 x 128 blocks along its rows, i.e. 128 x 1 blocks of x: what a
+ *            product that sums over x's rows reads.  lds >= rows, ldst >= cols.
+ *            128: 128 x 128 blocks; qt holds the same codes transposed,
+ *            scale_t the transposed scales.  lds >= ceil(cols / 128),
+ *            ldst >= ceil(rows / 128).
+ * q / scale, qt / scale_t  either pair may be NULL, not both.  x is read once
+ *            for both.  ldq >= cols, ldqt >= rows.
+ * Padding (columns past cols, scales past rows) is left as it was.
+ * Errors: INVALID_ARG (null pointers, sizes < 0, dtype, format, block_rows),
+ *         SHAPE (leading dimensions), ALIGNMENT (x, ldx, q, qt and theirs 16
+ *         bytes; scales 4), UNSUPPORTED (rows x ceil(cols / 128) >= 2^31).
+ */
+hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                             hif4_f8_format fmt, int32_t block_rows, uint8_t *q, int64_t ldq, float *scale,
+                             int64_t lds, uint8_t *qt, int64_t ldqt, float *scale_t, int64_t ldst,
+                             uint32_t *status, hif4_stream_t stream);
+
+/*
+ * hif4_gemm_f8_block — the product of block-scaled FP8 operands:
+ *   y[m][n] = bias[n] + sum over blocks u of K of
+ *             sa[u][m] sb[u, n] sum_{k in u} a[m][k] b[n][k]
+ * on the FP8 tensor cores, FP32 accumulation, the scales applied in FP32 per
+ * block, y rounded once.  Forward: a = activations, b = weight.  Input
+ * gradient: a = output gradient, b = the transposed weight codes.  Weight
+ * gradient: a, b = the transposed codes of the output gradient and of the
+ * input, both with 1 x 128 blocks (b_block_rows = 1).
+ * a     M x K codes (a_fmt, lda), sa 1 x 128 block scales (lds_a >= M).
+ * b     N x K codes (b_fmt, ldb), sb by b_block_rows: 128 = 128 x 128 blocks
+ *       (lds_b >= ceil(K / 128)), 1 = 1 x 128 blocks (lds_b >= N).
+ * The block-major scale arrays are 16-byte aligned, their leading dimensions
+ * multiples of 4 (they are read in 16-byte pieces; what lies between M or N
+ * and the next multiple of 4 never reaches y).
+ * bias  NULL or BF16 [N].   y  BF16 (FP32 with HIF4_LINEAR_OUT_F32, the only
+ *       flag) M x N, ldy.
+ * For one to a few rows of a the weight is streamed once, K split over a
+ * cluster of CTAs; the order of every sum is fixed.  Any M, N and K >= 1.
+ * A NaN code makes the outputs that it reaches NaN.
+ * Errors: SHAPE (K == 0 with M, N > 0; leading dimensions), ALIGNMENT,
+ *         INVALID_ARG, UNSUPPORTED (sizes, or a layout the driver's
+ *         tensor-map encoder refuses).  Bounded waits raise
+ *         HIF4_FLAG_TIMEOUT as hif4_gemm_bf16.
+ */
+hif4_status hif4_gemm_f8_block(const uint8_t *a, hif4_f8_format a_fmt, int64_t M, int64_t K, int64_t lda,
+                               const float *sa, int64_t lds_a, const uint8_t *b, hif4_f8_format b_fmt, int64_t N,
+                               int64_t ldb, const float *sb, int64_t lds_b, int32_t b_block_rows,
+                               const void *bias, void *y, int64_t ldy, uint32_t flags, uint32_t *status,
+                               hif4_stream_t stream);
+
+/*
+ * hif4_layer_norm — y = (x - mean) rstd gamma + beta per row, with
+ *   mean = sum x / cols,  var = sum (x - mean)^2 / cols,  rstd = 1 / sqrt(var + eps),
+ * statistics and arithmetic in FP32.
+ * x      rows x cols (F32 or BF16, ldx).  y  rows x cols (F32 or BF16, ldy).
+ * gamma, beta  NULL (1, 0) or [cols] of param_dtype, naturally aligned.
+ * mean, rstd   NULL or FP32 [rows] out: what the backward pass reads.
+ * eps >= 0 and finite.  NaN and infinities propagate as in the formulas.
+ * Errors: INVALID_ARG, SHAPE (ldx or ldy < cols), ALIGNMENT, UNSUPPORTED
+ *         (cols > 16384).
+ */
+hif4_status hif4_layer_norm(const void *x, hif4_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            const void *gamma, const void *beta, hif4_dtype param_dtype, float eps, void *y,
+                            hif4_dtype out_dtype, int64_t ldy, float *mean, float *rstd, hif4_stream_t stream);
+
+/*
+ * hif4_layer_norm_f8 — hif4_layer_norm whose FP32 result is quantized at
+ * once, in 1 x 128 blocks, into an operand of hif4_gemm_f8_block: bit for bit
+ * hif4_layer_norm with FP32 output followed by hif4_quantize_f8 with
+ * block_rows 1.  Arguments and errors as those two.
+ */
+hif4_status hif4_layer_norm_f8(const void *x, hif4_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               const void *gamma, const void *beta, hif4_dtype param_dtype, float eps,
+                               hif4_f8_format fmt, uint8_t *q, int64_t ldq, float *scale, int64_t lds, float *mean,
+                               float *rstd, uint32_t *status, hif4_stream_t stream);
+
+/*
+ * hif4_layer_norm_backward — with xh = (x - mean) rstd and w = dy gamma,
+ *   dx     = rstd (w - mean(w) - xh mean(w xh))      (means over the row),
+ *   dgamma = sum over rows of dy xh,   dbeta = sum over rows of dy.
+ * dy, x, dx  rows x cols of dtype (lddy, ldx, lddx); mean, rstd FP32 [rows] as
+ *            the forward call left them; gamma as there.
+ * dx, dgamma, dbeta  outputs, each may be NULL (not all); dgamma and dbeta
+ *            FP32 [cols], written (not added to), zero for rows == 0.
+ * workspace  >= hif4_layer_norm_backward_workspace(rows, cols) bytes, 256-byte
+ *            aligned, when dgamma or dbeta is wanted (the blocks' partial
+ *            sums, joined in a fixed order); calls that overlap on the GPU
+ *            need workspaces of their own.
+ * Errors: as hif4_layer_norm, and WORKSPACE.
+ */
+size_t hif4_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+hif4_status hif4_layer_norm_backward(const void *dy, int64_t lddy, const void *x, hif4_dtype dtype, int64_t rows,
+                                     int64_t cols, int64_t ldx, const float *mean, const float *rstd,
+                                     const void *gamma, hif4_dtype param_dtype, void *dx, int64_t lddx,
+                                     float *dgamma, float *dbeta, void *workspace, size_t ws_bytes,
+                                     hif4_stream_t stream);
 
 /*
  * hif4_ffn_w4a4 — the W4A4 HiF4 feed-forward block of a DiT layer [TA
