@@ -4,18 +4,26 @@
 // with 1 x 128 blocks on a and 128 x 128 or 1 x 128 blocks on b.
 //
 // FP32 scales cannot enter the tensor core (its block scales are powers of
-// two), so each 128-deep product goes to a TMEM accumulator of its own
-// (tcgen05 kind::f8f6f4, FP32 accumulation), and the promotion warps read it
-// back and add  scale * P  into FP32 totals held in registers: one FMA per
-// output element and 128 of K.
+// two), so each 128-deep product ("unit") goes to a TMEM accumulator of its own
+// (tcgen05 kind::f8f6f4, FP32 accumulation), and promotion warps read it back
+// and add  scale * P  into FP32 totals held in registers: one FMA per output
+// element and unit (two where b has a scale per row, whose product with a's is
+// formed in the same place).
 //
-// Roles (256 threads): warp 0 issues the TMA loads (128-byte swizzled operand
-// tiles into a ring, scale vectors into a ring of their own), warp 1 the MMAs
-// into two alternating accumulators; warps 4-7 promote.  The tile is 128 rows
-// of one operand (P) by BN rows of the other (Q).  SWAP exchanges the roles of
-// a and b: for few rows of a, the weight fills the MMA's 128 rows and the
-// tokens its narrow side, so that the tensor core and the TMA box do no work
-// for rows that do not exist.
+// Roles: warp 0 issues the TMA loads (128-byte swizzled operand tiles into a
+// ring), warps 1 and 2 the MMAs into two alternating accumulators, warp 3 the
+// copies of the scale vectors (a ring of their own, four units to a slot);
+// warps 4 and up promote.  A tile is 128 rows of one operand (P) by BN rows of
+// the other (Q).
+//   SWAP (BN 16, 32; up to 32 rows of a): the weight is P, so that it fills the
+//     MMA's 128 rows, and the tokens are Q.  Two CTAs per SM stream the weight:
+//     1 x 13824 x 5120 in 15.9 us, 4.5 TB/s, of which about 4 us are launch,
+//     first load and stores.
+//   128 x 128 tiles: short products of more rows.
+//   PAIR: 256 x 256 tiles of a cluster of two CTAs (tcgen05 cta_group::2).
+//     Each CTA loads 128 rows of P and 128 of Q, 32 KB a unit instead of the
+//     48 KB of a 128 x 256 tile: an SM takes in about 61 bytes a cycle, and a
+//     unit is 512 cycles of MMA.
 //
 // When there are too few tiles for the GPU, a cluster of S CTAs shares a tile:
 // each takes a contiguous part of K, leaves its FP32 totals in its shared
@@ -23,10 +31,19 @@
 // the CTAs in rank order (distributed shared memory).  The order of the sum is
 // fixed and no workspace is needed.
 //
+// What bounds the large products, measured at 57600 x 13824 x 5120: the 1 kW
+// power cap.  In a burst the pair kernel runs at 2157 TFLOP/s, sustained at
+// 1880 (1.53 GHz, about 1010 cycles a unit and pair of tiles); with the
+// promotion's FMAs left out in a trial copy it sustained 2126, without its TMEM
+// reads as well 2352, so about a fifth of the energy is the promotion, which
+// the FP32 scales cost.  A 128 x 256 tile of one CTA measured 3 to 8 % slower.
+//
 // Every mbarrier wait is bounded (4 s); a role that gives up sets the block's
-// abort flag, the producer lets its copies land, the MMA thread drains its
+// abort flag, the producers let their copies land, the MMA warps drain their
 // MMAs before TMEM is freed, every thread still meets the cluster barriers,
 // and HIF4_FLAG_TIMEOUT is raised.
+#include <mutex>
+
 #include "hif4_f8.cuh"
 #include "hif4_pdl.cuh"
 #include "hif4_sm100.cuh"
@@ -38,39 +55,55 @@ bool make_tensor_map_u8_2d_sw128(CUtensorMap *map, const void *base, uint64_t in
 
 namespace gemm8b {
 
-constexpr int BP = 128;                         // rows of a tile (MMA M)
+constexpr int BP = 128;                         // rows of a CTA's tile (MMA M, of each CTA)
 constexpr int KU = 128;                         // K elements (bytes) per unit and per stage
-constexpr int SLOTS = 8;                        // scale ring
+constexpr int SG = 4;                           // units per slot of the scale ring
+constexpr int SLOTS = 2;
+constexpr int ST_BYTES = 2048;                 // a promotion warp's staging of its stores: 32 rows of 64 bytes
 constexpr int GROUP = 16;                       // raster: P tiles per group
 constexpr uint64_t TIMEOUT_NS = 4000000000ull;
+constexpr uint64_t DRAIN_NS = 100000000ull;
 
-template <int BN>
+// BN: columns of the tile.  PAIR: two CTAs share a tile of 256 rows (each holds 128 of them and half of
+// Q's rows).
+template <int BN, bool VECB, bool PAIR, bool SWAP>
 struct Cfg {
-    static constexpr int EPI_WARPS = 4;
+    static constexpr int EPI_WGS = BN >= 128 ? 2 : 1;                 // promotion warpgroups
+    static constexpr bool SPLITS = !PAIR && BN <= 128;                // may share K over a cluster
+    static constexpr int EPI_WARPS = 4 * EPI_WGS;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    static constexpr int ACC = BN;              // totals per promotion thread
-    static constexpr int CTAS = BN <= 32 ? 3 : BN <= 64 ? 2 : 1;      // per SM
-    static constexpr int STAGES = BN <= 32 ? 3 : BN <= 64 ? 4 : 5;
-    static constexpr int CH = BN >= 128 ? 32 : 16;                    // columns per TMEM read
+    static constexpr int ACC = BN / EPI_WGS;    // totals per promotion thread
+    static constexpr int CTAS = BN <= 32 ? 2 : 1;                // per SM
+    static constexpr int STAGES = PAIR ? 6 : 5;
+    static constexpr int CH = 16;                // columns per TMEM read
+    static constexpr int NCH = ACC / CH;
+    // registers: the promotion warps take what the producer's warpgroup gives back; the shares add up to
+    // what the launch brings along, 384 threads x 168
+    static constexpr int REG_LOW = BN >= 256 ? 72 : 0;
+    static constexpr int REG_HIGH = BN >= 256 ? 216 : 0;
     static constexpr int P_BYTES = BP * KU;
-    static constexpr int Q_BYTES = BN * KU;
+    static constexpr int Q_BYTES = BN * KU / (PAIR ? 2 : 1);
     static constexpr int RING = STAGES * (P_BYTES + Q_BYTES);
     static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int PITCH = BP + 1;        // of the staged totals: conflict-free along either axis
-    static constexpr int BARS = 2 * STAGES + 4 + 1 + SLOTS;
-    static constexpr size_t SMEM = (size_t)RING + SLOTS * (BP + BN) * 4 + BARS * 8 + 64 + 1024;
-    static_assert(SLOTS >= STAGES + 3, "a scale slot is rewritten only after its unit's promotion");
-    static_assert(BN * PITCH * 4 <= RING, "the staged totals reuse the operand ring");
+    static constexpr int BARS = 2 * STAGES + 4 + 2 + 2 * SLOTS;
+    static constexpr bool PVEC = !SWAP || VECB, QVEC = SWAP || VECB;  // P / Q carry scale vectors
+    static constexpr int PV = PVEC ? SLOTS * SG * BP : 0, QV = QVEC ? SLOTS * SG * BN : 0;
+    static constexpr int STORE = SWAP ? 0 : EPI_WARPS * ST_BYTES;
+    static constexpr size_t SMEM = (size_t)RING + STORE + (PV + QV) * 4 + BARS * 8 + 64 + 1024;
+    static_assert(!SPLITS || (SWAP ? BN * (BP + 4) : BP * (BN + 4)) * 4 <= RING,
+                  "the staged totals reuse the operand ring");
+    static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
 
 struct Args {
     int P, Q;                                   // rows of the two operands
     int num_p, num_q, num_u, num_tiles;
-    int split;                                  // CTAs per tile (the cluster)
+    int split;                                  // CTAs that share a tile's K (the cluster)
     const float *p_vec, *q_vec;                 // scale vectors [num_u][ld] (null: block scales)
     int64_t p_ld, q_ld;
     const float *blk;                           // 128 x 128 block scales [row block][num_u ..]
     int64_t blk_ld;
+    int blk_rows;
     const uint16_t *bias;                       // BF16 [N], nullable
     void *y;
     int64_t ldy;
@@ -120,13 +153,28 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ float peer_ld(uint32_t local, uint32_t rank)
+__device__ __forceinline__ float4 peer_ld4(uint32_t local, uint32_t rank)
 {
     uint32_t a;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_dec()
+{
+    if constexpr (N > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc()
+{
+    if constexpr (N > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void tile_coords(int t, const Args &g, int &pb, int &qb)
@@ -138,6 +186,55 @@ __device__ __forceinline__ void tile_coords(int t, const Args &g, int &pb, int &
     const int r = t - gi * per_group;
     pb = first + r % gp;
     qb = r / gp;
+}
+
+// Stores the N totals of each of a warp's 32 rows (r0 + lane), W columns (64 bytes) at a time.
+template <int N, int W, bool F32>
+__device__ __forceinline__ void store_rows(const Args &g, uint8_t *st, const float (&acc)[N], int lane, int64_t r0,
+                                           int q0)
+{
+    constexpr int E = F32 ? 4 : 2;
+    const int row = lane >> 2, piece = lane & 3;
+#pragma unroll
+    for (int j = 0; j < N; j += W) {
+        if (q0 + j >= g.Q) break;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 w;
+            const float *v = acc + j + i * (W / 4);
+            if (F32)
+                w = make_uint4(f_bits(v[0]), f_bits(v[1]), f_bits(v[2]), f_bits(v[3]));
+            else
+                w = make_uint4(f8::pack_bf16_rn(v[0], v[1]), f8::pack_bf16_rn(v[2], v[3]),
+                               f8::pack_bf16_rn(v[F32 ? 0 : 4], v[F32 ? 0 : 5]),
+                               f8::pack_bf16_rn(v[F32 ? 0 : 6], v[F32 ? 0 : 7]));
+            *reinterpret_cast<uint4 *>(st + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = w;
+        }
+        __syncwarp();
+        const int col = q0 + j + piece * (W / 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = row + i * 8;
+            const uint4 w = *reinterpret_cast<const uint4 *>(st + r * 64 + ((piece ^ (r >> 1)) & 3) * 16);
+            if (r0 + r < g.P) {
+                uint8_t *dst = static_cast<uint8_t *>(g.y) + ((r0 + r) * g.ldy + col) * E;
+                if (col + W / 4 <= g.Q) {
+                    *reinterpret_cast<uint4 *>(dst) = w;
+                } else {
+                    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < W / 4; ++k)
+                        if (col + k < g.Q) {
+                            if (F32)
+                                reinterpret_cast<uint32_t *>(dst)[k] = a[k & 3];
+                            else
+                                reinterpret_cast<uint16_t *>(dst)[k] = (uint16_t)(a[(k >> 1) & 3] >> (16 * (k & 1)));
+                        }
+                }
+            }
+        }
+    }
 }
 
 // acc[0..N) += r c[0..N) p[0..N); COLS: column factors from shared memory, else r alone.
@@ -167,32 +264,50 @@ __device__ __forceinline__ void store_one(const Args &g, int64_t m, int n, float
     }
 }
 
+// The first `valid` of 4 values at columns n .. n + 3 (n a multiple of 4).
+__device__ __forceinline__ void store4(const Args &g, int64_t m, int n, const float (&v)[4], int valid)
+{
+    if (valid >= 4) {
+        if (g.out_f32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(g.y) + m * g.ldy + n) =
+                make_float4(v[0], v[1], v[2], v[3]);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.y) + m * g.ldy + n) =
+                make_uint2(f8::pack_bf16_rn(v[0], v[1]), f8::pack_bf16_rn(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < valid) store_one(g, m, n + k, v[k]);
+    }
+}
+
 __device__ __forceinline__ float bias_of(const Args &g, int n)
 {
     return g.bias ? bits_f((uint32_t)__ldg(g.bias + n) << 16) : 0.0f;
 }
 
-template <int BN, bool SWAP, bool VECB>
-__global__ void __launch_bounds__(Cfg<BN>::THREADS, Cfg<BN>::CTAS)
+template <int BN, bool SWAP, bool VECB, bool PAIR>
+__global__ void __launch_bounds__(Cfg<BN, VECB, PAIR, SWAP>::THREADS, Cfg<BN, VECB, PAIR, SWAP>::CTAS)
 k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, Args g)
 {
     using namespace sm100;
-    using C = Cfg<BN>;
-    constexpr bool PVEC = !SWAP || VECB;        // P / Q carry scale vectors
-    constexpr bool QVEC = SWAP || VECB;
+    using C = Cfg<BN, VECB, PAIR, SWAP>;
+    constexpr bool PVEC = C::PVEC, QVEC = C::QVEC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sP = smem;
     uint8_t *sQ = sP + C::STAGES * C::P_BYTES;
-    float *sPv = reinterpret_cast<float *>(smem + C::RING);               // [SLOTS][BP]
-    float *sQv = sPv + SLOTS * BP;                                        // [SLOTS][BN]
-    uint64_t *full = reinterpret_cast<uint64_t *>(sQv + SLOTS * BN);
+    uint8_t *sSt = smem + C::RING;
+    float *sPv = reinterpret_cast<float *>(sSt + C::STORE);               // [SLOTS][SG][BP]
+    float *sQv = sPv + C::PV;                                             // [SLOTS][SG][BN]
+    uint64_t *full = reinterpret_cast<uint64_t *>(sQv + C::QV);
     uint64_t *empty = full + C::STAGES;
     uint64_t *tfull = empty + C::STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
-    uint64_t *sfull = drain + 1;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sfull + SLOTS);
+    uint64_t *sfull = drain + 2;
+    uint64_t *sempty = sfull + SLOTS;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sempty + SLOTS);
     volatile uint32_t *abort_flag = tmem_holder + 1;
 
     const int warp = threadIdx.x >> 5;
@@ -205,58 +320,73 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], C::EPI_WARPS);
+            mbar_init(&tempty[a], C::EPI_WARPS * (PAIR ? 2 : 1));
+            mbar_init(&drain[a], 1);
         }
-        for (int s = 0; s < SLOTS; ++s) mbar_init(&sfull[s], 1);
-        mbar_init(drain, 1);
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&sfull[s], 1);
+            mbar_init(&sempty[s], C::EPI_WARPS);
+        }
         *abort_flag = 0u;
         fence_barrier_init();
         prefetch_tensormap(&tmP);
         prefetch_tensormap(&tmQ);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_holder, C::TMEM_COLS);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(tmem_holder, C::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_holder, C::TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
+    if (PAIR) cluster_sync();                   // the barriers of both CTAs are ready
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     pdl_enter();
 
-    const int split = g.split;
-    const int rank = split > 1 ? (int)cluster_rank() : 0;
-    const int t0 = blockIdx.x / split, tstep = gridDim.x / split;
-    const int u0 = (int)((int64_t)g.num_u * rank / split), u1 = (int)((int64_t)g.num_u * (rank + 1) / split);
+    const int split = C::SPLITS ? g.split : 1;
+    const int rank = PAIR || split > 1 ? (int)cluster_rank() : 0;
+    const int share = PAIR ? 2 : split;         // CTAs per tile
+    const int t0 = blockIdx.x / share, tstep = gridDim.x / share;
+    const int u0 = PAIR ? 0 : (int)((int64_t)g.num_u * rank / split);
+    const int u1 = PAIR ? g.num_u : (int)((int64_t)g.num_u * (rank + 1) / split);
+    const int p_of = PAIR ? 2 : 1, p_at = PAIR ? rank : 0;                // this CTA's 128 rows of a tile
 
     if (warp < 4) {
-        if (warp == 0 && lane == 0) {
-            // ---------------------------------------------------- producer
-            uint32_t stage = 0, phase = 0, issued = 0, ug = 0;
+        reg_dec<C::REG_LOW>();
+        if (warp == 0) {
+            // ---------------------------------------------------- operands
+            uint32_t stage = 0, phase = 0, issued = 0;
             bool ok = true;
             for (int t = t0; ok && t < g.num_tiles; t += tstep) {
                 int pb, qb;
                 tile_coords(t, g, pb, qb);
-                const uint32_t pv = (uint32_t)min(BP, (g.P - pb * BP + 3) & ~3) * 4;
-                const uint32_t qv = (uint32_t)min(BN, (g.Q - qb * BN + 3) & ~3) * 4;
-                for (int u = u0; u < u1; ++u, ++ug) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, g.timeout_ns)) {
+                const int prow = (pb * p_of + p_at) * BP, qrow = qb * BN + (PAIR ? rank * (BN / 2) : 0);
+                for (int u = u0; u < u1; ++u) {
+                    if (!mbar_wait_spin(&empty[stage], phase ^ 1u, abort_flag, g.timeout_ns)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[stage], C::P_BYTES + C::Q_BYTES);
-                    if (!(g.withhold && blockIdx.x == 0 && ug == 0))      // else its wait can only run out
-                        tma_load_2d(sP + stage * C::P_BYTES, &tmP, u * KU, pb * BP, &full[stage]);
-                    tma_load_2d(sQ + stage * C::Q_BYTES, &tmQ, u * KU, qb * BN, &full[stage]);
-                    // the slot's previous unit lies at least STAGES + 3 back: this stage's last MMAs were
-                    // issued after every warp had released the accumulator of the unit two before them,
-                    // and with it had done the promotion of the unit before that
-                    const uint32_t slot = ug % SLOTS;
-                    mbar_arrive_expect_tx(&sfull[slot], (PVEC ? pv : 0u) + (QVEC ? qv : 0u));
-                    if (PVEC)
-                        bulk_load(sPv + slot * BP, g.p_vec + u * g.p_ld + (int64_t)pb * BP, pv, &sfull[slot]);
-                    if (QVEC)
-                        bulk_load(sQv + slot * BN, g.q_vec + u * g.q_ld + (int64_t)qb * BN, qv, &sfull[slot]);
+                    if (elect_one()) {
+                        // a withheld copy's wait can only run out
+                        const bool skip = g.withhold && blockIdx.x == 0 && issued == 0;
+                        if (PAIR) {
+                            // both CTAs' copies complete on the issuing CTA's barrier
+                            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (C::P_BYTES + C::Q_BYTES));
+                            const uint32_t bar = peer_addr(smem_addr(&full[stage]), 0);
+                            if (!skip) tma_load_2d_pair(sP + stage * C::P_BYTES, &tmP, u * KU, prow, bar);
+                            tma_load_2d_pair(sQ + stage * C::Q_BYTES, &tmQ, u * KU, qrow, bar);
+                        } else {
+                            mbar_arrive_expect_tx(&full[stage], C::P_BYTES + C::Q_BYTES);
+                            if (!skip) tma_load_2d(sP + stage * C::P_BYTES, &tmP, u * KU, prow, &full[stage]);
+                            tma_load_2d(sQ + stage * C::Q_BYTES, &tmQ, u * KU, qrow, &full[stage]);
+                        }
+                    }
+                    __syncwarp();
                     ++issued;
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -264,39 +394,100 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     }
                 }
             }
-            if (!ok) {
-                // let our own copies land before the block leaves
+            if (PAIR && ok) {
+                // the issuing CTA's arrivals on this CTA's barriers come in before it leaves
                 for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
                     const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
                     const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-                    mbar_wait_bounded(&full[s], ph, nullptr, 100000000ull);
-                }
-                for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
-                    const uint32_t u = ug - 1 - i;
-                    mbar_wait_bounded(&sfull[u % SLOTS], (u / SLOTS) & 1u, nullptr, 100000000ull);
+                    mbar_wait_bounded(&empty[s], ph, abort_flag, g.timeout_ns);
                 }
             }
-        } else if (warp == 1 && lane == 0) {
-            // ---------------------------------------------------- MMA issuer
-            uint32_t stage = 0, phase = 0, ug = 0;
+            if (!ok) {
+                // let our own copies land before the block leaves; a pair's second CTA cannot see the
+                // barrier that its copies complete on, and waits the same time
+                for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
+                    const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
+                    const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
+                    mbar_wait_bounded(&full[s], ph, nullptr, DRAIN_NS);
+                    if (PAIR && rank > 0) break;
+                }
+            }
+        } else if (warp == 3) {
+            // ---------------------------------------------------- scales
+            // A slot holds those of SG consecutive units of a tile (the last one of a tile maybe fewer).
+            uint32_t slot = 0, phase = 0;
             bool ok = true;
             for (int t = t0; ok && t < g.num_tiles; t += tstep) {
-                for (int u = u0; u < u1; ++u, ++ug) {
-                    const uint32_t b = ug & 1u;
-                    if (!mbar_wait_bounded(&tempty[b], ((ug >> 1) & 1u) ^ 1u, abort_flag, g.timeout_ns) ||
-                        !mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns)) {
+                int pb, qb;
+                tile_coords(t, g, pb, qb);
+                const int prow = (pb * p_of + p_at) * BP, qrow = qb * BN;
+                // (a pair's second CTA may lie past the last row; it then has nothing to read)
+                const int pn = max(0, min(BP, (g.P - prow + 3) & ~3)), qn = min(BN, (g.Q - qrow + 3) & ~3);
+                for (int u = u0; u < u1; u += SG) {
+                    if (!mbar_wait_spin(&sempty[slot], phase ^ 1u, abort_flag, g.timeout_ns)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t p0 = smem_addr(sP + stage * C::P_BYTES);
-                    const uint32_t q0 = smem_addr(sQ + stage * C::Q_BYTES);
+                    if (elect_one()) {
+                        const int n = min(SG, u1 - u);
+                        mbar_arrive_expect_tx(&sfull[slot], (uint32_t)(n * ((PVEC ? pn : 0) + (QVEC ? qn : 0)) * 4));
+                        for (int i = 0; i < n; ++i) {
+                            if (PVEC && pn > 0)
+                                bulk_load(sPv + (slot * SG + i) * BP, g.p_vec + (u + i) * g.p_ld + prow, pn * 4,
+                                          &sfull[slot]);
+                            if (QVEC)
+                                bulk_load(sQv + (slot * SG + i) * BN, g.q_vec + (u + i) * g.q_ld + qrow, qn * 4,
+                                          &sfull[slot]);
+                        }
+                    }
+                    __syncwarp();
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok)                            // let the copies in flight land
+                for (uint32_t s = 0; s < (uint32_t)SLOTS; ++s)
+                    mbar_wait_bounded(&sfull[s], s < slot ? phase : (phase ^ 1u), nullptr, DRAIN_NS);
+        } else if (!PAIR || rank == 0) {
+            // ---------------------------------------------------- MMA issuers
+            // One warp for each accumulator: issuing a unit's MMAs and commits takes one thread as long
+            // as the tensor core takes to run them, so the two take turns.  The loop is warp-uniform and
+            // one elected lane issues.
+            const uint32_t b = warp - 1;
+            uint32_t stage = 0, phase = 0, tph = 1;
+            const uint64_t pd0 = smem_desc_sw128(smem_addr(sP)), qd0 = smem_desc_sw128(smem_addr(sQ));
+            const uint32_t d = tmem_base + b * BN;
+            bool ok = true;
+            for (int t = t0; ok && t < g.num_tiles; t += tstep) {
+                for (int u = u0; u < u1; ++u) {
+                    if (((uint32_t)(u - u0) & 1u) == b) {
+                        if (!mbar_wait_spin(&tempty[b], tph, abort_flag, g.timeout_ns) ||
+                            !mbar_wait_spin(&full[stage], phase, abort_flag, g.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tph ^= 1u;
+                        tc_fence_after();
+                        const uint64_t pd = pd0 + stage * (C::P_BYTES / 16), qd = qd0 + stage * (C::Q_BYTES / 16);
+                        if (elect_one()) {
+                            if (PAIR) {
 #pragma unroll
-                    for (int k = 0; k < KU / 32; ++k)
-                        mma_f8f6f4(tmem_base + b * BN, smem_desc_sw128(p0 + k * 32), smem_desc_sw128(q0 + k * 32),
-                                   g.idesc, (uint32_t)k);
-                    mma_commit(&empty[stage]);
-                    mma_commit(&tfull[b]);
+                                for (int k = 0; k < KU / 32; ++k)
+                                    mma_f8f6f4_pair(d, pd + 2 * k, qd + 2 * k, g.idesc, k > 0);
+                                mma_commit_pair(&tfull[b]);
+                                mma_commit_pair(&empty[stage]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < KU / 32; ++k)
+                                    mma_f8f6f4(d, pd + 2 * k, qd + 2 * k, g.idesc, k > 0);
+                                mma_commit(&tfull[b]);
+                                mma_commit(&empty[stage]);
+                            }
+                        }
+                        __syncwarp();
+                    }
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -304,127 +495,169 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 }
             }
             // no MMA may still be running when TMEM is released
-            mma_commit(drain);
-            mbar_wait_bounded(drain, 0, nullptr, 100000000ull);
+            if (elect_one()) {
+                if (PAIR)
+                    mma_commit_pair_local(&drain[b]);
+                else
+                    mma_commit(&drain[b]);
+            }
+            __syncwarp();
+            mbar_wait_bounded(&drain[b], 0, nullptr, DRAIN_NS);
         }
         __syncwarp();
-        if (split > 1) {
+        if (C::SPLITS && split > 1) {
             cluster_sync();
             cluster_sync();
         }
     } else {
         // ------------------------------------------------------- promotion
+        reg_inc<C::REG_HIGH>();
         const int q4 = warp & 3;                         // TMEM lane quarter
-        const int prow = q4 * 32 + lane;                 // this thread's row of the tile
-        uint32_t ug = 0;
+        const int prow = q4 * 32 + lane;                 // this thread's row of the CTA's tile
+        const int c0 = (warp / 4 - 1) * C::ACC;          // and its first column
+        const uint32_t ta = tmem_base + ((uint32_t)(q4 * 32) << 16) + c0;
+        const uint32_t rel = PAIR ? peer_addr(smem_addr(tempty), 0) : smem_addr(tempty);   // of the issuing CTA
+        uint32_t slot = 0, sphase = 0, tph0 = 0, tph1 = 0;
         bool ok = true;
         for (int t = t0; ok && t < g.num_tiles; t += tstep) {
             int pb, qb;
             tile_coords(t, g, pb, qb);
+            pb = pb * p_of + p_at;
             float acc[C::ACC];
 #pragma unroll
             for (int j = 0; j < C::ACC; ++j) acc[j] = 0.0f;
-            // block scales: of the tile's 128 rows of b (SWAP: P; BN <= 128 columns lie in one block)
-            const float *blk = VECB ? nullptr : g.blk + (SWAP ? pb : (qb * BN) / 128) * g.blk_ld;
-            float bs = VECB || u0 >= u1 ? 1.0f : __ldg(blk + u0);
-            for (int u = u0; u < u1; ++u, ++ug) {
-                const float bcur = bs;
-                if (!VECB && u + 1 < u1) bs = __ldg(blk + u + 1);
-                const uint32_t slot = ug % SLOTS, b = ug & 1u;
-                if (!mbar_wait_bounded(&sfull[slot], (ug / SLOTS) & 1u, abort_flag, g.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                float r = PVEC ? sPv[slot * BP + prow] : 1.0f;
-                if (!VECB) r *= bcur;
-                const float *cv = sQv + slot * BN;
-                if (!mbar_wait_bounded(&tfull[b], (ug >> 1) & 1u, abort_flag, g.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t ta = tmem_base + ((uint32_t)(q4 * 32) << 16) + b * BN;
-                uint32_t d0[C::CH], d1[C::CH];
-                tmem_load<C::CH>(ta, d0);
-                tmem_landed<C::CH>(d0);
+            // block scales: of the tile's 128 rows of b (SWAP: P; ACC <= 128 columns lie in one block)
+            const float *blk =
+                VECB ? nullptr : g.blk + min(SWAP ? pb : (qb * BN + c0) / 128, g.blk_rows - 1) * g.blk_ld;
+            // Lane l holds those of units u0 + 32 i + l: a global load for each unit would cost its whole
+            // latency, since the wait for the accumulator's reads waits for it too.
+            float bs = 1.0f;
+            for (int u = u0; u < u1; u += SG) {
+                if (!VECB && ((u - u0) & 31) == 0) bs = u + lane < u1 ? __ldg(blk + u + lane) : 0.0f;
+                ok = mbar_wait_spin(&sfull[slot], sphase, abort_flag, g.timeout_ns);
+                float rc[SG];
 #pragma unroll
-                for (int c = 0; c < C::ACC; c += 2 * C::CH) {
-                    const bool two = c + C::CH < C::ACC, more = c + 2 * C::CH < C::ACC;
-                    if (two) tmem_load<C::CH>(ta + c + C::CH, d1);
-                    if (!two) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[b]);
-                    }
-                    promote<C::CH, QVEC>(acc + c, d0, r, cv + c);
-                    if (two) {
-                        tmem_landed<C::CH>(d1);
-                        if (more) {
-                            tmem_load<C::CH>(ta + c + 2 * C::CH, d0);
-                        } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&tempty[b]);
+                for (int i = 0; i < SG; ++i) {
+                    rc[i] = PVEC ? sPv[(slot * SG + i) * BP + prow] : 1.0f;
+                    if (!VECB) rc[i] *= __shfl_sync(0xFFFFFFFFu, bs, ((u - u0) & 31) + i);
+                }
+                const float *cv = sQv + slot * SG * BN + c0;
+                // Unrolled over the group, so that the accumulator of each unit is known at compile time.
+#pragma unroll
+                for (int i = 0; i < SG; ++i) {
+                    if (u + i < u1) {
+                        constexpr int odd[4] = {0, 1, 0, 1};
+                        const uint32_t b = odd[i & 3];
+                        uint32_t &tph = b ? tph1 : tph0;
+                        // (after a time-out the group is finished on whatever lies there, and then left)
+                        ok &= mbar_wait_spin(&tfull[b], tph, abort_flag, g.timeout_ns);
+                        tph ^= 1u;
+                        tc_fence_after();
+                        // One chunk in flight for each warp: the two warps of a scheduler take turns at
+                        // reading and adding.
+#pragma unroll
+                        for (int c = 0; c < C::NCH; ++c) {
+                            uint32_t d[C::CH];
+                            tmem_load<C::CH>(ta + b * BN + c * C::CH, d);
+                            tmem_landed<C::CH>(d);
+                            if (c + 1 == C::NCH) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) {
+                                    if (PAIR)
+                                        mbar_arrive_remote(rel + b * 8);
+                                    else
+                                        mbar_arrive(&tempty[b]);
+                                }
+                            }
+                            promote<C::CH, QVEC>(acc + c * C::CH, d, rc[i], cv + i * BN + c * C::CH);
                         }
-                        promote<C::CH, QVEC>(acc + c + C::CH, d1, r, cv + c + C::CH);
-                        if (more) tmem_landed<C::CH>(d0);
                     }
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty[slot]);
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    sphase ^= 1u;
                 }
             }
             if (!ok) break;
             const int p = pb * BP + prow;
-            const int q0 = qb * BN;
-            if (split > 1) {
-                // the last unit's MMAs have completed: nothing reads or writes the ring any more
+            const int q0 = qb * BN + c0;
+            if (C::SPLITS && split > 1) {
+                // the last unit's MMAs have completed: nothing reads or writes the ring any more.
+                // Staged along y's contiguous axis, with a pitch that keeps 16-byte accesses free of
+                // bank conflicts
                 float *st = reinterpret_cast<float *>(smem);
+                if (SWAP) {
 #pragma unroll
-                for (int j = 0; j < C::ACC; ++j) st[j * C::PITCH + prow] = acc[j];
+                    for (int j = 0; j < C::ACC; ++j) st[(c0 + j) * (BP + 4) + prow] = acc[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < C::ACC; j += 4)
+                        *reinterpret_cast<float4 *>(st + prow * (BN + 4) + c0 + j) =
+                            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                }
             } else if (SWAP) {
                 const float bv = p < g.P ? bias_of(g, p) : 0.0f;
 #pragma unroll
                 for (int j = 0; j < C::ACC; ++j)
                     if (p < g.P && q0 + j < g.Q) store_one(g, q0 + j, p, acc[j] + bv);
-            } else if (p < g.P) {
+            } else {
                 if (g.bias) {
 #pragma unroll
                     for (int j = 0; j < C::ACC; ++j)
                         if (q0 + j < g.Q) acc[j] += bias_of(g, q0 + j);
                 }
-                if (q0 + C::ACC <= g.Q) {
-#pragma unroll
-                    for (int j = 0; j < C::ACC; j += 8) {
-                        float o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = acc[j + i];
-                        if (g.out_f32)
-                            f8::store8<false>(g.y, (int64_t)p * g.ldy + q0 + j, o, 8);
-                        else
-                            f8::store8<true>(g.y, (int64_t)p * g.ldy + q0 + j, o, 8);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < C::ACC; ++j)
-                        if (q0 + j < g.Q) store_one(g, p, q0 + j, acc[j]);
-                }
+            }
+            if (!SWAP && !(C::SPLITS && split > 1)) {
+                // Rows leave through shared memory, 64 bytes of each of the warp's 32 rows at a time, so
+                // that a store writes 8 rows x 64 bytes (whole sectors) and not 32 x 16.  16-byte piece i
+                // of row r sits at piece i ^ (r / 2 % 4): no bank conflicts either way.
+                uint8_t *st = sSt + (warp - 4) * ST_BYTES;
+                const int64_t r0 = (int64_t)pb * BP + q4 * 32;
+                if (g.out_f32)
+                    store_rows<C::ACC, 16, true>(g, st, acc, lane, r0, q0);
+                else
+                    store_rows<C::ACC, 32, false>(g, st, acc, lane, r0, q0);
             }
         }
         __syncwarp();
-        if (split > 1) {
+        if (C::SPLITS && split > 1) {
             cluster_sync();
             if (ok && t0 < g.num_tiles) {
                 int pb, qb;
                 tile_coords(t0, g, pb, qb);
                 const uint32_t st = smem_addr(smem);
-                const int share = BP * BN / split;
-                for (int i = (int)threadIdx.x - 128; i < share; i += 32 * C::EPI_WARPS) {
-                    const int e = rank * share + i;
-                    // consecutive lanes along n, the contiguous axis of y
-                    const int r = SWAP ? e % BP : e / BN, c = SWAP ? e / BP : e % BN;
-                    float s = 0.0f;
-                    for (int k = 0; k < split; ++k) s += peer_ld(st + (c * C::PITCH + r) * 4, (uint32_t)k);
-                    const int pp = pb * BP + r, qq = qb * BN + c;
-                    if (pp < g.P && qq < g.Q)
-                        store_one(g, SWAP ? qq : pp, SWAP ? pp : qq, s + bias_of(g, SWAP ? pp : qq));
+                // pieces of 4 along y's contiguous axis; rank r adds up the r-th part of them
+                constexpr int INNER = SWAP ? BP : BN;
+                const int pieces = BP * BN / 4;
+                const int p1 = pieces * (rank + 1) / split;
+                for (int i = pieces * rank / split + (int)threadIdx.x - 128; i < p1; i += 32 * C::EPI_WARPS) {
+                    const int e = i * 4;
+                    const int o = e / INNER, in = e % INNER;
+                    const uint32_t addr = st + (o * (INNER + 4) + in) * 4;
+                    float4 part[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < split) part[k] = peer_ld4(addr, (uint32_t)k);
+                    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < split) {
+                            v[0] += part[k].x;
+                            v[1] += part[k].y;
+                            v[2] += part[k].z;
+                            v[3] += part[k].w;
+                        }
+                    const int m = (SWAP ? qb * BN : pb * BP) + o, n = (SWAP ? pb * BP : qb * BN) + in;
+                    if (m < (SWAP ? g.Q : g.P)) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (n + k < (SWAP ? g.P : g.Q)) v[k] += bias_of(g, n + k);
+                        store4(g, m, n, v, (SWAP ? g.P : g.Q) - n);
+                    }
                 }
             }
             cluster_sync();
@@ -432,10 +665,47 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     }
 
     tc_fence_before();
+    if (PAIR) cluster_sync();                   // neither CTA's memory is used by the other any more
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if (warp == 1) {
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
     if (threadIdx.x == 0 && *abort_flag) status_or(g.status, HIF4_FLAG_TIMEOUT);
+}
+
+// Clusters of `size` CTAs that fit on the device at once (cached per kernel, size and device).
+int resident_clusters(const void *kernel, cudaLaunchConfig_t cfg, int size)
+{
+    struct Entry {
+        const void *kernel;
+        int size, dev, n;
+    };
+    static std::mutex mu;
+    static Entry table[256];
+    static int used = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < used; ++i)
+        if (table[i].kernel == kernel && table[i].size == size && table[i].dev == dev) return table[i].n;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    if (used < 256) table[used++] = Entry{kernel, size, dev, n};
+    return n;
 }
 
 struct Call {
@@ -446,14 +716,15 @@ struct Call {
     bool a_e5m2, b_e5m2;
 };
 
-template <int BN, bool SWAP, bool VECB>
+template <int BN, bool SWAP, bool VECB, bool PAIR>
 hif4_status launch(const Call &c, Args g, cudaStream_t stream)
 {
-    using CF = Cfg<BN>;
+    using CF = Cfg<BN, VECB, PAIR, SWAP>;
     const uint8_t *p = SWAP ? c.b : c.a, *q = SWAP ? c.a : c.b;
     g.P = (int)(SWAP ? c.N : c.M);
     g.Q = (int)(SWAP ? c.M : c.N);
-    g.num_p = (g.P + BP - 1) / BP;
+    constexpr int TP = PAIR ? 2 * BP : BP;       // rows of a tile
+    g.num_p = (g.P + TP - 1) / TP;
     g.num_q = (g.Q + BN - 1) / BN;
     g.num_u = (int)f8::blocks_of(c.K);
     if ((int64_t)g.num_p * g.num_q > INT32_MAX / 8) return HIF4_ERR_UNSUPPORTED;
@@ -464,39 +735,56 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
     g.q_ld = SWAP ? c.lds_a : c.lds_b;
     g.blk = VECB ? nullptr : c.sb;
     g.blk_ld = c.lds_b;
-    g.idesc = sm100::idesc_f8_f32(BP, BN, SWAP ? c.b_e5m2 : c.a_e5m2, SWAP ? c.a_e5m2 : c.b_e5m2);
+    g.blk_rows = (int)f8::blocks_of(c.N);
+    g.idesc = sm100::idesc_f8_f32(TP, BN, SWAP ? c.b_e5m2 : c.a_e5m2, SWAP ? c.a_e5m2 : c.b_e5m2);
 
     CUtensorMap tmP, tmQ;
     if (!make_tensor_map_u8_2d_sw128(&tmP, p, (uint64_t)c.K, (uint64_t)g.P, (uint64_t)(SWAP ? c.ldb : c.lda), KU,
                                      BP) ||
         !make_tensor_map_u8_2d_sw128(&tmQ, q, (uint64_t)c.K, (uint64_t)g.Q, (uint64_t)(SWAP ? c.lda : c.ldb), KU,
-                                     BN))
+                                     PAIR ? BN / 2 : BN))
         return HIF4_ERR_UNSUPPORTED;            // the driver's encoder refused the layout
-    auto k = k_gemm_f8_block<BN, SWAP, VECB>;
+    auto k = k_gemm_f8_block<BN, SWAP, VECB, PAIR>;
+    if (CF::REG_HIGH > 0) {
+        // the promotion warps wait for registers that the launch must have brought along
+        static const bool enough = [&] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, k) == cudaSuccess &&
+                   at.numRegs * CF::THREADS >= 128 * CF::REG_LOW + 32 * CF::EPI_WARPS * CF::REG_HIGH;
+        }();
+        if (!enough) return HIF4_ERR_UNSUPPORTED;
+    }
     // cheap enough to set on every call, and then right on every device
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CF::SMEM);
     if (e != cudaSuccess) return cuda_failed(e);
 
-    const int slots = sm_count() * CF::CTAS;
-    int split = 1;
-    while (split < 8 && (int64_t)g.num_tiles * split * 2 <= slots && g.num_u >= split * 2 * 4) split *= 2;
-    g.split = split;
-    int64_t grid = (int64_t)g.num_tiles * split;
-    if (split == 1 && grid > slots) grid = slots;
-
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(CF::THREADS);
     cfg.dynamicSmemBytes = CF::SMEM;
     cfg.stream = stream;
+    int split = 1;
+    if (CF::SPLITS) {
+        // K is shared by as many CTAs as can all be resident at once, while each keeps at least 8 units:
+        // with fewer, filling the ring and joining the parts costs more than it saves (1 x 5120 x 5120,
+        // 40 units: 12.7 us on 1 CTA a tile, 9.4 on 2, 8.6 on 3 or 4, 8.8 on 5 or 6, 13.3 on 8, whose
+        // clusters no longer fit beside one another).
+        for (int s = 2; s <= 8 && g.num_u >= 8 * s && (int64_t)g.num_tiles * s <= (int64_t)sm_count() * CF::CTAS; ++s)
+            if (resident_clusters(reinterpret_cast<const void *>(k), cfg, s) >= g.num_tiles) split = s;
+    }
+    g.split = split;
+    const int cluster = PAIR ? 2 : split;
+    int64_t grid = (int64_t)g.num_tiles * cluster;
+    const int64_t slots = (int64_t)sm_count() * CF::CTAS / cluster * cluster;
+    if (split == 1 && grid > slots) grid = slots;       // persistent
+    cfg.gridDim = dim3((unsigned)grid);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t le = cudaLaunchKernelEx(&cfg, k, tmP, tmQ, g);
     if (le != cudaSuccess) {
         (void)cudaGetLastError();
@@ -508,10 +796,21 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
 template <bool VECB>
 hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
 {
-    if (c.M <= 16) return launch<16, true, VECB>(c, g, s);
-    if (c.M <= 32) return launch<32, true, VECB>(c, g, s);
-    if (c.M <= 64) return launch<64, true, VECB>(c, g, s);
-    return launch<128, false, VECB>(c, g, s);
+    if (c.M <= 16) return launch<16, true, VECB, false>(c, g, s);
+    if (c.M <= 32) return launch<32, true, VECB, false>(c, g, s);
+    // 128 x 128 tiles of one CTA or 256 x 256 tiles of a pair, by estimated time in ns: a wave of tiles
+    // costs its units and its stores.  The pair's unit takes longer but is four times the work and needs
+    // half the operand bytes per product; the smaller tiles fill the SMs better and may share K.  Measured
+    // (us, small / pair): 128 x 5120 x 5120 12.8 / 23.8, 512 x 5120 x 13824 67.6 / 57.1, 1024 x 5120 x 5120
+    // 41.5 / 45.4, 1024 x 13824 x 5120 83.2 / 73.3, 8192 x 13824 x 5120 620 / 560.
+    const int64_t units = f8::blocks_of(c.K), sms = sm_count();
+    const int64_t small = f8::blocks_of(c.M) * f8::blocks_of(c.N);
+    const int64_t wide = ((c.M + 255) / 256) * ((c.N + 255) / 256);
+    const int64_t share = small * 2 > sms ? 1 : sms / small < 8 ? sms / small : 8;
+    const int64_t t_small = ((small + sms - 1) / sms) * (units / share * 290 + 1500);
+    const int64_t t_wide = ((wide * 2 + sms - 1) / sms) * (units * 490 + 1800);
+    if (t_wide < t_small) return launch<256, false, VECB, true>(c, g, s);
+    return launch<128, false, VECB, false>(c, g, s);
 }
 
 } // namespace gemm8b

@@ -135,7 +135,9 @@ def operand(H, rng, rows, K, fmt, block):
 
 GEMMS = [(1, 128, 128), (1, 1, 1), (1, 300, 1000), (2, 256, 4096), (7, 100, 129), (16, 512, 640), (17, 130, 640),
          (32, 257, 2048), (33, 384, 100), (64, 1000, 512), (65, 128, 128), (100, 300, 777), (128, 256, 1152),
-         (129, 129, 64), (200, 333, 1000), (256, 512, 512), (300, 264, 2048), (513, 640, 384)]
+         (129, 129, 64), (200, 333, 1000), (256, 512, 512), (300, 264, 2048), (513, 640, 384),
+         # many short tiles: the CTA pairs; 2305 = 9 x 256 + 1 leaves a pair's second CTA without a row
+         (2305, 2817, 129), (2560, 2500, 300), (2400, 2600, 1024)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMMS)
@@ -161,7 +163,7 @@ def test_product_matches_the_definition(H, M, N, K, block):
         assert_only_view_written(raw, view)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (16, 300, 2000), (200, 300, 4096)])
+@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (16, 300, 2000), (200, 300, 4096), (2560, 2500, 300)])
 def test_product_is_the_same_every_time(H, M, N, K):
     import torch
     rng = np.random.default_rng(11)
@@ -192,7 +194,7 @@ def test_bounded_waits_of_the_product(H):
     import torch
     from block_floating_point_hif4_b200 import binding as B
     rng = np.random.default_rng(13)
-    for M, N, K in ((1, 512, 4096), (300, 300, 512)):
+    for M, N, K in ((1, 512, 4096), (300, 300, 512), (2560, 2500, 300)):
         a, sa, av, sav = operand(H, rng, M, K, "e4m3", 1)
         b, sb, bv, sbv = operand(H, rng, N, K, "e4m3", 128)
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
