@@ -24,30 +24,50 @@ constexpr float kTiny = 7.888609052210118e-31f; // 2^-100
 
 __host__ __device__ constexpr float fmt_max(int fmt) { return fmt == HIF4_E5M2 ? 57344.0f : 448.0f; }
 
-struct ScalePair {
-    float scale, factor;
-};
-
-__device__ __forceinline__ ScalePair scale_pair(float amax, float fmax)
+// One of the two, from the bits of the maximum: a warp forms both in one go, the
+// scale in some lanes and the factor in others.  Either quotient
+// takes about as long as encoding eight elements.
+__device__ __forceinline__ float scale_or_factor(uint32_t amax_bits, float fmax, bool scale)
 {
-    const float a = fmaxf(amax, kTiny);
-    return ScalePair{__fdiv_rn(a, fmax), __fdiv_rn(fmax, a)};
+    const float a = fmaxf(bits_f(amax_bits), kTiny);
+    return __fdiv_rn(scale ? a : fmax, scale ? fmax : a);
 }
 
 // Two codes, lo in the low byte (round to nearest even, saturating).
-__device__ __forceinline__ uint32_t cvt2(float lo, float hi, bool e5m2)
+template <bool E5M2>
+__device__ __forceinline__ uint32_t cvt2(float lo, float hi)
 {
     uint16_t r;
-    if (e5m2)
+    if (E5M2)
         asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     else
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d, bool e5m2)
+// Codes of a f and b f (one packed FP32 product).
+template <bool E5M2>
+__device__ __forceinline__ uint32_t encode2(float a, float b, float f)
 {
-    return cvt2(a, b, e5m2) | cvt2(c, d, e5m2) << 16;
+    float x, y;
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(f));
+    return cvt2<E5M2>(x, y);
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float f)
+{
+    return encode2<E5M2>(a, b, f) | encode2<E5M2>(c, d, f) << 16;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // NaN -> 0, +-Inf -> +-FLT_MAX over a granule; *bad set when it did.  One test
@@ -169,13 +189,30 @@ __device__ __forceinline__ void store_codes8(uint8_t *p, uint32_t lo, uint32_t h
     }
 }
 
-__device__ __forceinline__ float amax8(const float (&v)[8])
+// Bits of the largest magnitude of a granule (as FP32; NaN above Inf above
+// every finite value).  BF16: on pairs of 15-bit keys.
+template <bool BF16>
+__device__ __forceinline__ uint32_t amax_bits(const Raw8<BF16> &r)
 {
-    float m = 0.0f;
+    if (BF16) {
+        const uint32_t m = max_u16x2(max_u16x2(r.w[0].x & 0x7FFF7FFFu, r.w[0].y & 0x7FFF7FFFu),
+                                     max_u16x2(r.w[0].z & 0x7FFF7FFFu, r.w[0].w & 0x7FFF7FFFu));
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+    const uint4 a = r.w[0], b = r.w[BF16 ? 0 : 1];
+    return max(max(max(a.x & 0x7FFFFFFFu, a.y & 0x7FFFFFFFu), max(a.z & 0x7FFFFFFFu, a.w & 0x7FFFFFFFu)),
+               max(max(b.x & 0x7FFFFFFFu, b.y & 0x7FFFFFFFu), max(b.z & 0x7FFFFFFFu, b.w & 0x7FFFFFFFu)));
+}
+
+__device__ __forceinline__ uint32_t amax_bits(const float (&v)[8])
+{
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) m = max(m, f_bits(v[i]) & 0x7FFFFFFFu);
     return m;
 }
+
+constexpr uint32_t kInfBits = 0x7F800000u;
 
 inline bool valid_fmt(int fmt) { return fmt == HIF4_E4M3 || fmt == HIF4_E5M2; }
 inline int64_t blocks_of(int64_t n) { return (n + BLK - 1) / BLK; }

@@ -3,8 +3,8 @@
 // HBM-bound streaming kernels: every input element is read once, whatever
 // layouts are asked for, and every code byte and scale written once.
 //
-//   k_f8_rows   1 x 128 blocks, row-major codes only: 16 lanes own a block,
-//               8 elements each; four xor-shuffles give its maximum.
+//   k_f8_rows   1 x 128 blocks, row-major codes only: 8 lanes own a block,
+//               16 elements each.
 //   k_f8_tile   everything else: one 128 x 128 tile per CTA, an 8 x 8 piece
 //               per thread in registers, so that row maxima, column maxima
 //               and the tile's maximum all come from one read.  The
@@ -30,40 +30,58 @@ struct F8QuantArgs {
     int64_t ldst;
     uint32_t nblk;             // column blocks
     FastDiv nblk_div;
-    uint32_t items;            // k_f8_rows: rows x nblk
+    uint32_t items;            // k_f8_rows: strips of 32 rows x nblk
     uint32_t *status;
     float fmax;
-    bool e5m2;
 };
 
 constexpr int kThreads = 256;
+constexpr int kRowsPerCta = kThreads / 8;      // k_f8_rows: rows of a 128-column strip that a block takes at once
 
-template <bool BF16>
+// 1 x 128 blocks, row-major codes.  Eight lanes own a block: two granules each,
+// 64 elements apart, so that a load of the eight covers 128 consecutive bytes
+// of BF16.  The 32 groups of a CTA take one 128-column strip of 32 consecutive
+// rows, whose scales are 32 consecutive floats.
+template <bool BF16, bool E5M2>
 __global__ void __launch_bounds__(kThreads) k_f8_rows(F8QuantArgs a)
 {
-    const int l16 = threadIdx.x & 15;
-    uint32_t bad = 0;
-    const uint32_t stride = gridDim.x * (kThreads / 16);
-    // all lanes of a warp take the same number of trips (shuffles below)
-    const uint32_t first = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 5) * 2;
-    for (uint32_t w = first; w < a.items; w += stride) {
-        const uint32_t it = w + ((threadIdx.x >> 4) & 1);
-        const bool live = it < a.items;
-        const uint32_t row = live ? a.nblk_div.div(it) : 0;
-        const uint32_t blk = live ? it - row * a.nblk : 0;
-        const int64_t col = (int64_t)blk * BLK + l16 * 8;
-        const int valid = live ? (int)max((int64_t)0, min((int64_t)8, a.cols - col)) : 0;
-        float v[8];
-        widen8<BF16>(load_raw8<BF16>(a.x, (int64_t)row * a.ldx + col, valid), v);
-        sanitize_all(v, bad);
-        float m = amax8(v);
+    const int l8 = threadIdx.x & 7, group = threadIdx.x >> 3;
+    bool bad = false;
+    for (uint32_t it = blockIdx.x; it < a.items; it += gridDim.x) {
+        const uint32_t strip = a.nblk_div.div(it);
+        const uint32_t blk = it - strip * a.nblk;
+        const int64_t row = (int64_t)strip * kRowsPerCta + group;
+        const int64_t col = (int64_t)blk * BLK + l8 * 8;
+        const bool live = row < a.rows;
+        const int v0 = live ? (int)max((int64_t)0, min((int64_t)8, a.cols - col)) : 0;
+        const int v1 = live ? (int)max((int64_t)0, min((int64_t)8, a.cols - col - 64)) : 0;
+        const int64_t off = row * a.ldx + col;
+        Raw8<BF16> r0 = load_raw8<BF16>(a.x, off, v0), r1 = load_raw8<BF16>(a.x, off + 64, v1);
+        uint32_t m = max(amax_bits<BF16>(r0), amax_bits<BF16>(r1));
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const ScalePair sp = scale_pair(m, a.fmax);
-        const uint32_t lo = cvt4(v[0] * sp.factor, v[1] * sp.factor, v[2] * sp.factor, v[3] * sp.factor, a.e5m2);
-        const uint32_t hi = cvt4(v[4] * sp.factor, v[5] * sp.factor, v[6] * sp.factor, v[7] * sp.factor, a.e5m2);
-        if (valid > 0) store_codes8(a.q + (int64_t)row * a.ldq + col, lo, hi, valid);
-        if (live && l16 == 0) a.scale[(int64_t)blk * a.lds + row] = sp.scale;
+        for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        float x[2][8];
+        widen8<BF16>(r0, x[0]);
+        widen8<BF16>(r1, x[1]);
+        if (__any_sync(0xFFFFFFFFu, m >= kInfBits)) {            // rare: map what is not finite, and again
+            uint32_t mapped = 0;
+            sanitize_all(x[0], mapped);
+            sanitize_all(x[1], mapped);
+            bad |= mapped != 0;
+            m = max(amax_bits(x[0]), amax_bits(x[1]));
+#pragma unroll
+            for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        }
+        const float s = scale_or_factor(m, a.fmax, l8 & 1);
+        const float f = __shfl_sync(0xFFFFFFFFu, s, 0, 8);
+        uint8_t *q = a.q + row * a.ldq + col;
+        if (v0 > 0)
+            store_codes8(q, encode4<E5M2>(x[0][0], x[0][1], x[0][2], x[0][3], f),
+                         encode4<E5M2>(x[0][4], x[0][5], x[0][6], x[0][7], f), v0);
+        if (v1 > 0)
+            store_codes8(q + 64, encode4<E5M2>(x[1][0], x[1][1], x[1][2], x[1][3], f),
+                         encode4<E5M2>(x[1][4], x[1][5], x[1][6], x[1][7], f), v1);
+        if (live && l8 == 1) a.scale[(int64_t)blk * a.lds + row] = s;
     }
     if (bad) status_or(a.status, HIF4_FLAG_NONFINITE);
 }
@@ -79,13 +97,27 @@ __device__ __forceinline__ uint4 staged16(const uint8_t *sT, int c, int c16)
     return (s & 1) ? make_uint4(w.z, w.w, w.x, w.y) : w;
 }
 
-// SQUARE: 128 x 128 blocks (both layouts share the tile's scale); otherwise
+// 4 x 4 bytes: word i holds row i; -> word j holds column j.
+__device__ __forceinline__ void transpose4(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d)
+{
+    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);   // a0 b0 a1 b1, a2 b2 a3 b3
+    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+    a = __byte_perm(ab0, cd0, 0x5410);
+    b = __byte_perm(ab0, cd0, 0x7632);
+    c = __byte_perm(ab1, cd1, 0x5410);
+    d = __byte_perm(ab1, cd1, 0x7632);
+}
+
+// SQUARE: 128 x 128 blocks (both layouts hold the same codes); otherwise
 // 1 x 128 blocks row-wise and 128 x 1 blocks for the transposed codes.
-template <bool BF16, bool SQUARE>
+// Thread (rg, cg) = (t / 16, t % 16) owns rows 8 rg .. and columns 8 cg .. of
+// the tile.
+template <bool BF16, bool SQUARE, bool E5M2>
 __global__ void __launch_bounds__(kThreads) k_f8_tile(F8QuantArgs a)
 {
     __shared__ __align__(16) uint8_t sT[BLK * BLK];
-    __shared__ float sMax[kThreads / 32][BLK];
+    __shared__ __align__(16) uint32_t sMax[kThreads / 32][BLK];
+    __shared__ __align__(16) float sF[BLK];
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5;
     const uint32_t rb = a.nblk_div.div(blockIdx.x);
     const uint32_t cb = blockIdx.x - rb * a.nblk;
@@ -95,100 +127,172 @@ __global__ void __launch_bounds__(kThreads) k_f8_tile(F8QuantArgs a)
     const int rvalid = (int)max((int64_t)0, min((int64_t)8, a.rows - r0));
 
     float v[8][8];
+    uint32_t rmax[8];
     {
         Raw8<BF16> raw[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) raw[i] = load_raw8<BF16>(a.x, (r0 + i) * a.ldx + c0, i < rvalid ? cvalid : 0);
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) widen8<BF16>(raw[i], v[i]);
+        for (int i = 0; i < 8; ++i) {
+            rmax[i] = amax_bits<BF16>(raw[i]);
+            m = max(m, rmax[i]);
+            widen8<BF16>(raw[i], v[i]);
+        }
+        if (m >= kInfBits) {                                     // rare
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sanitize_all(v[i], bad);
+                rmax[i] = amax_bits(v[i]);
+            }
+            status_or(a.status, HIF4_FLAG_NONFINITE);
+        }
     }
-    uint32_t bad = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sanitize_all(v[i], bad);
-    if (bad) status_or(a.status, HIF4_FLAG_NONFINITE);
 
-    float tile_factor = 0.0f;
+    float f[8];                                                  // factors: of the rows, then of the columns
     if (SQUARE) {
-        float m = 0.0f;
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, amax8(v[i]));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
         if ((threadIdx.x & 31) == 0) sMax[warp][0] = m;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, sMax[w][0]);
-        const ScalePair sp = scale_pair(m, a.fmax);
-        tile_factor = sp.factor;
-        if (threadIdx.x == 0) {
-            if (a.q) a.scale[(int64_t)rb * a.lds + cb] = sp.scale;
-            if (a.qt) a.scale_t[(int64_t)cb * a.ldst + rb] = sp.scale;
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, sMax[w][0]);
+        const float s = scale_or_factor(m, a.fmax, cg & 1);
+        const float t = __shfl_sync(0xFFFFFFFFu, s, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = t;
+        if (threadIdx.x == 1) {
+            if (a.q) a.scale[(int64_t)rb * a.lds + cb] = s;
+            if (a.qt) a.scale_t[(int64_t)cb * a.ldst + rb] = s;
         }
+    } else if (a.q) {
+        // The 16 lanes of a row group hold parts of the same 8 rows: halving exchanges leave lane bits
+        // 3..1 with the maximum of row (bits 3..1), and bit 0 chooses the quotient that the lane forms.
+        uint32_t k4[4], k2[2], k1;
+        const bool b3 = cg & 8, b2 = cg & 4, b1 = cg & 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, b3 ? rmax[i] : rmax[i + 4], 8);
+            k4[i] = max(b3 ? rmax[i + 4] : rmax[i], other);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, b2 ? k4[i] : k4[i + 2], 4);
+            k2[i] = max(b2 ? k4[i + 2] : k4[i], other);
+        }
+        {
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, b1 ? k2[0] : k2[1], 2);
+            k1 = max(b1 ? k2[1] : k2[0], other);
+        }
+        k1 = max(k1, __shfl_xor_sync(0xFFFFFFFFu, k1, 1));
+        const float s = scale_or_factor(k1, a.fmax, cg & 1);
+        const int row = cg >> 1;
+        if ((cg & 1) && row < rvalid) a.scale[(int64_t)cb * a.lds + r0 + row] = s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __shfl_sync(0xFFFFFFFFu, s, 2 * i, 16);
     }
-    if (a.q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f = tile_factor;
-            if (!SQUARE) {
-                float m = amax8(v[i]);
-#pragma unroll
-                for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                const ScalePair sp = scale_pair(m, a.fmax);
-                f = sp.factor;
-                if (cg == 0 && i < rvalid) a.scale[(int64_t)cb * a.lds + r0 + i] = sp.scale;
-            }
-            const uint32_t lo = cvt4(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f, a.e5m2);
-            const uint32_t hi = cvt4(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f, a.e5m2);
-            if (i < rvalid && cvalid > 0) store_codes8(a.q + (r0 + i) * a.ldq + c0, lo, hi, cvalid);
-        }
-    }
-    if (a.qt) {
-        if (!SQUARE) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i][j]));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                if ((threadIdx.x & 31) < 16) sMax[warp][cg * 8 + j] = m;
-            }
-            __syncthreads();
-        }
+    if (!SQUARE && a.qt) {
+        // column maxima: over the thread's rows, the warp's two row groups, then the warps
+        uint32_t cm[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float f = tile_factor;
-            if (!SQUARE) {
-                float m = 0.0f;
+            cm[j] = 0;
 #pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, sMax[w][cg * 8 + j]);
-                const ScalePair sp = scale_pair(m, a.fmax);
-                f = sp.factor;
-                if (rg == 0 && j < cvalid) a.scale_t[(int64_t)rb * a.ldst + c0 + j] = sp.scale;
-            }
-            const uint32_t lo = cvt4(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f, a.e5m2);
-            const uint32_t hi = cvt4(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f, a.e5m2);
-            *reinterpret_cast<uint2 *>(sT + (cg * 8 + j) * BLK + ((rg ^ cg) * 8)) = make_uint2(lo, hi);
+            for (int i = 0; i < 8; ++i) cm[j] = max(cm[j], f_bits(v[i][j]) & 0x7FFFFFFFu);
+            cm[j] = max(cm[j], __shfl_xor_sync(0xFFFFFFFFu, cm[j], 16));
+        }
+        if ((threadIdx.x & 31) < 16) {
+            *reinterpret_cast<uint4 *>(&sMax[warp][cg * 8]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+            *reinterpret_cast<uint4 *>(&sMax[warp][cg * 8 + 4]) = make_uint4(cm[4], cm[5], cm[6], cm[7]);
         }
         __syncthreads();
-        const int64_t rbase = (int64_t)rb * BLK;
+        const int c = threadIdx.x & (BLK - 1);
+        uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < BLK * BLK / 16 / kThreads; ++k) {
-            const int p = threadIdx.x + k * kThreads;
-            const int c = p >> 3, c16 = p & 7;
-            const int64_t col = (int64_t)cb * BLK + c;
-            const int64_t row = rbase + c16 * 16;
-            if (col < a.cols && row < a.rows) {
-                const uint4 w = staged16(sT, c, c16);
-                uint8_t *dst = a.qt + col * a.ldqt + row;
-                if (row + 16 <= a.rows) {
-                    *reinterpret_cast<uint4 *>(dst) = w;
-                } else {
-                    store_codes8(dst, w.x, w.y, (int)min((int64_t)8, a.rows - row));
-                    if (a.rows - row > 8) store_codes8(dst + 8, w.z, w.w, (int)(a.rows - row - 8));
-                }
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, sMax[w][c]);
+        const bool want_scale = threadIdx.x >= BLK;              // the two halves form one quotient each
+        const float s = scale_or_factor(m, a.fmax, want_scale);
+        const int64_t col = (int64_t)cb * BLK + c;
+        if (!want_scale)
+            sF[c] = s;
+        else if (col < a.cols)
+            a.scale_t[(int64_t)rb * a.ldst + col] = s;
+    }
+
+    uint32_t w0[8], w1[8];                                       // codes of the thread's rows
+    if (SQUARE || a.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w0[i] = encode4<E5M2>(v[i][0], v[i][1], v[i][2], v[i][3], f[i]);
+            w1[i] = encode4<E5M2>(v[i][4], v[i][5], v[i][6], v[i][7], f[i]);
+            if (a.q && i < rvalid && cvalid > 0) store_codes8(a.q + (r0 + i) * a.ldq + c0, w0[i], w1[i], cvalid);
+        }
+    }
+    if (!a.qt) return;
+    if (SQUARE) {
+        transpose4(w0[0], w0[1], w0[2], w0[3]);
+        transpose4(w0[4], w0[5], w0[6], w0[7]);
+        transpose4(w1[0], w1[1], w1[2], w1[3]);
+        transpose4(w1[4], w1[5], w1[6], w1[7]);
+    } else {
+        __syncthreads();                                         // sF is complete
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = sF[cg * 8 + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t lo, hi;                                         // column j: rows 0..3, 4..7
+        if (SQUARE) {
+            lo = j < 4 ? w0[j & 3] : w1[j & 3];
+            hi = j < 4 ? w0[4 + (j & 3)] : w1[4 + (j & 3)];
+        } else {
+            lo = encode4<E5M2>(v[0][j], v[1][j], v[2][j], v[3][j], f[j]);
+            hi = encode4<E5M2>(v[4][j], v[5][j], v[6][j], v[7][j], f[j]);
+        }
+        *reinterpret_cast<uint2 *>(sT + (cg * 8 + j) * BLK + ((rg ^ cg) * 8)) = make_uint2(lo, hi);
+    }
+    __syncthreads();
+    const int64_t rbase = (int64_t)rb * BLK;
+#pragma unroll
+    for (int k = 0; k < BLK * BLK / 16 / kThreads; ++k) {
+        const int p = threadIdx.x + k * kThreads;
+        const int c = p >> 3, c16 = p & 7;
+        const int64_t col = (int64_t)cb * BLK + c;
+        const int64_t row = rbase + c16 * 16;
+        if (col < a.cols && row < a.rows) {
+            const uint4 w = staged16(sT, c, c16);
+            uint8_t *dst = a.qt + col * a.ldqt + row;
+            if (row + 16 <= a.rows) {
+                *reinterpret_cast<uint4 *>(dst) = w;
+            } else {
+                store_codes8(dst, w.x, w.y, (int)min((int64_t)8, a.rows - row));
+                if (a.rows - row > 8) store_codes8(dst + 8, w.z, w.w, (int)(a.rows - row - 8));
             }
         }
     }
+}
+
+template <bool BF16, bool E5M2>
+hif4_status launch_quant(F8QuantArgs &a, bool square, cudaStream_t s)
+{
+    const int64_t cblk = a.nblk;
+    if (!square && !a.qt) {
+        const int64_t items = (a.rows + kRowsPerCta - 1) / kRowsPerCta * cblk;
+        a.items = (uint32_t)items;
+        const void *k = reinterpret_cast<const void *>(k_f8_rows<BF16, E5M2>);
+        const int64_t most = 4 * (int64_t)sm_count() * blocks_per_sm(k, kThreads, 0);
+        k_f8_rows<BF16, E5M2><<<(unsigned)(items < most ? items : most), kThreads, 0, s>>>(a);
+        return launch_status();
+    }
+    const unsigned grid = (unsigned)(f8::blocks_of(a.rows) * cblk);
+    if (square)
+        k_f8_tile<BF16, true, E5M2><<<grid, kThreads, 0, s>>>(a);
+    else
+        k_f8_tile<BF16, false, E5M2><<<grid, kThreads, 0, s>>>(a);
+    return launch_status();
 }
 
 } // namespace
@@ -232,32 +336,10 @@ extern "C" hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t
     a.ldst = ldst;
     a.nblk = (uint32_t)cblk;
     a.nblk_div = FastDiv((uint32_t)cblk);
-    a.items = (uint32_t)(rows * cblk);
     a.status = status;
     a.fmax = f8::fmt_max(fmt);
-    a.e5m2 = fmt == HIF4_E5M2;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!square && !qt) {
-        int64_t grid = ((int64_t)a.items + kThreads / 16 - 1) / (kThreads / 16);
-        const int64_t most = 32 * (int64_t)sm_count();
-        if (grid > most) grid = most;
-        if (dtype == HIF4_BF16)
-            k_f8_rows<true><<<(unsigned)grid, kThreads, 0, s>>>(a);
-        else
-            k_f8_rows<false><<<(unsigned)grid, kThreads, 0, s>>>(a);
-        return launch_status();
-    }
-    const unsigned grid = (unsigned)(rblk * cblk);
-    if (dtype == HIF4_BF16) {
-        if (square)
-            k_f8_tile<true, true><<<grid, kThreads, 0, s>>>(a);
-        else
-            k_f8_tile<true, false><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (square)
-            k_f8_tile<false, true><<<grid, kThreads, 0, s>>>(a);
-        else
-            k_f8_tile<false, false><<<grid, kThreads, 0, s>>>(a);
-    }
-    return launch_status();
+    if (dtype == HIF4_BF16)
+        return fmt == HIF4_E5M2 ? launch_quant<true, true>(a, square, s) : launch_quant<true, false>(a, square, s);
+    return fmt == HIF4_E5M2 ? launch_quant<false, true>(a, square, s) : launch_quant<false, false>(a, square, s);
 }

@@ -186,21 +186,31 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads) k_norm_fwd(NormAr
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (i >= n) y[i] = 0.0f;
-                sanitize_all(y, bad);
-                float m = amax8(y);
+                constexpr int W = LANES < 16 ? LANES : 16;       // lanes of a 128-block
+                uint32_t m = amax_bits(y);
 #pragma unroll
-                for (int o = (LANES < 16 ? LANES : 16) / 2; o; o >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                const ScalePair sp = scale_pair(m, a.fmax);
-                const bool e5 = a.e5m2 != 0;
-                const uint32_t lo =
-                    cvt4(y[0] * sp.factor, y[1] * sp.factor, y[2] * sp.factor, y[3] * sp.factor, e5);
-                const uint32_t hi =
-                    cvt4(y[4] * sp.factor, y[5] * sp.factor, y[6] * sp.factor, y[7] * sp.factor, e5);
+                for (int o = W / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                if (__any_sync(0xFFFFFFFFu, m >= kInfBits)) {    // rare: map what is not finite, and again
+                    sanitize_all(y, bad);
+                    m = amax_bits(y);
+#pragma unroll
+                    for (int o = W / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                }
+                const float s = scale_or_factor(m, a.fmax, t & 1);
+                const float f = __shfl_sync(0xFFFFFFFFu, s, 0, W);
+                uint32_t lo, hi;
+                if (a.e5m2) {
+                    lo = encode4<true>(y[0], y[1], y[2], y[3], f);
+                    hi = encode4<true>(y[4], y[5], y[6], y[7], f);
+                } else {
+                    lo = encode4<false>(y[0], y[1], y[2], y[3], f);
+                    hi = encode4<false>(y[4], y[5], y[6], y[7], f);
+                }
                 if (n > 0) {
                     store_codes8(static_cast<uint8_t *>(a.y) + row * a.ldy + col, lo, hi, n);
-                    if (col % BLK == 0) a.scale[(int64_t)(col / BLK) * a.lds + row] = sp.scale;
                 }
+                // the block's second lane holds the scale
+                if (live && t % W == 1 && col - 8 < a.cols) a.scale[(int64_t)(col / BLK) * a.lds + row] = s;
             }
         }
     }
