@@ -212,6 +212,20 @@ __device__ __forceinline__ uint32_t amax_bits(const float (&v)[8])
     return m;
 }
 
+// Largest magnitude, NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float amax8_nan(const float (&v)[8])
+{
+    return max_nan(max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))),
+                   max_nan(max_nan(fabsf(v[4]), fabsf(v[5])), max_nan(fabsf(v[6]), fabsf(v[7]))));
+}
+
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 inline bool valid_fmt(int fmt) { return fmt == HIF4_E4M3 || fmt == HIF4_E5M2; }

@@ -2,12 +2,16 @@
 // and backward (input gradient, and the reduction of the weight's and bias's
 // gradients).
 //
-// A row of C elements belongs to a group of T threads (8 or 32 lanes, or a
+// A row of C elements belongs to a group of T threads (8 to 32 lanes, or a
 // whole block); thread t owns the 8-element granules t, t + T, ... (at most V
-// of them) and keeps them in registers, so x (and dy) are read once.  The
-// granules' columns are the same for every row a thread meets: gamma and beta,
-// and in the backward pass the column sums, stay in registers for the life of
-// a block, and a block takes rows b, b + grid, ...
+// of them), so x (and dy) are read once.  The granules' columns are the same
+// for every row a thread meets: gamma and beta, and in the backward pass the
+// column sums, stay in registers for the life of a block, and a block takes
+// rows b, b + grid, ...
+//
+// A thread fetches its own granules up to three rows ahead with cp.async into
+// its own places of shared memory: no barrier, no registers for data in flight,
+// and a granule that the row ends in is filled up with zeros by the copy.
 //
 // Forward statistics, in FP32: each warp takes its sum, then its sum of
 // squares about the warp's own mean, and the warps' (n, mean, M2) are merged
@@ -29,10 +33,11 @@ namespace {
 using namespace f8;
 
 constexpr int kMaxCols = 16384;
+constexpr int kMaxRows = 1 << 30;        // row numbers plus a grid's rows stay below 2^31
 constexpr int kSmallThreads = 256;       // block size of the sub-warp and one-warp rows
 constexpr int kMaxPartials = 592;        // most blocks of the backward kernel (4 per SM of 148)
 
-enum NormOut { OUT_BF16 = 0, OUT_F32 = 1, OUT_F8 = 2 };
+enum NormOut { OUT_BF16 = 0, OUT_F32 = 1, OUT_E4M3 = 2, OUT_E5M2 = 3 };
 
 struct NormArgs {
     const void *x;
@@ -43,10 +48,8 @@ struct NormArgs {
     float inv_cols, eps;
     void *y;                     // BF16 / FP32 / FP8 codes
     int64_t ldy;
-    float *scale;                // OUT_F8
+    float *scale;                // FP8 outputs
     int64_t lds;
-    float fmax;
-    uint32_t e5m2;
     float *mean, *rstd;          // nullable
     uint32_t *status;
 };
@@ -63,20 +66,144 @@ struct NormBwdArgs {
     float inv_cols;
     void *dx;                    // nullable
     int64_t lddx;
-    float *part;                 // [blocks][2][cols]; null when neither sum is wanted
+    float *part;                 // [blocks][2][cols rounded up to 8]; null when neither sum is wanted
 };
 
-// The 8 parameters of a granule (naturally aligned; loaded once per block).
-__device__ __forceinline__ void load_params(const void *p, uint32_t bf16, int col, int valid, float dflt,
-                                            float (&v)[8])
+// ---- packed FP32 pairs (one instruction for two elements)
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 pack2(float lo, float hi)
 {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v)
+{
+    const float2 p = unpack2(v);
+    return p.x + p.y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen8(const Raw8<BF16> &r, f2 (&v)[4])
+{
+    float e[8];
+    f8::widen8<BF16>(r, e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = dflt;
-        if (p && i < valid)
-            v[i] = bf16 ? bits_f((uint32_t)static_cast<const uint16_t *>(p)[col + i] << 16)
-                        : static_cast<const float *>(p)[col + i];
+    for (int i = 0; i < 4; ++i) v[i] = pack2(e[2 * i], e[2 * i + 1]);
+}
+
+// The 8 parameters of a granule (naturally aligned; loaded once per block).
+__device__ __forceinline__ void load_params(const void *p, uint32_t bf16, int col, int valid, float dflt, f2 (&v)[4])
+{
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = dflt;
+    if (p && valid >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        if (bf16)
+            f8::widen8<true>(load_raw8<true>(p, col, 8), e);
+        else
+            f8::widen8<false>(load_raw8<false>(p, col, 8), e);
+    } else if (p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid)
+                e[i] = bf16 ? bits_f((uint32_t)static_cast<const uint16_t *>(p)[col + i] << 16)
+                            : static_cast<const float *>(p)[col + i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack2(e[2 * i], e[2 * i + 1]);
+}
+
+// Sum over the first nw lanes (the others hold 0), given to all.
+__device__ __forceinline__ float warps_sum(float v, int nw)
+{
+    if (nw > 16) v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    if (nw > 8) v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+    if (nw > 4) v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+    if (nw > 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+    return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
+// ---- the rows in flight: `depth` stages of [piece][thread] 16-byte pieces, each
+// written and read by its thread alone.  Four stages (60 KB in flight per SM for
+// rows of 5120 BF16), fewer where wide rows leave no room.
+template <bool BF16>
+constexpr int pieces() { return BF16 ? 1 : 2; }
+
+template <bool BF16>
+constexpr int depth(int wide, int v, int arrays)
+{
+    const int stage = arrays * v * pieces<BF16>() * (wide ? wide : kSmallThreads) * 16;
+    // shared memory of a CTA: one, two or three of them to an SM
+    const int room = (wide > 320 || (!wide && v > 2) ? 200 : wide == 160 ? 68 : 104) * 1024;
+    return stage * 4 <= room ? 4 : stage * 2 <= room ? 2 : 1;
+}
+
+// L1: through the first-level cache, for the FP32 pieces, two of which share a
+// 32-byte sector that each would otherwise fetch from L2.
+template <bool L1>
+__device__ __forceinline__ void async16(uint4 *dst, const void *src, int bytes)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if (L1)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+}
+
+// Starts the copy of a granule; elements from `valid` on become 0 (nothing is read for valid = 0).
+template <bool BF16>
+__device__ __forceinline__ void fetch8(uint4 *dst, int threads, const uint8_t *src, int valid)
+{
+    if (BF16) {
+        async16<false>(dst, src, valid * 2);
+    } else {
+        async16<true>(dst, src, min(valid, 4) * 4);
+        async16<true>(dst + threads, valid > 4 ? src + 16 : src, max(valid - 4, 0) * 4);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> fetched8(const uint4 *src, int threads)
+{
+    Raw8<BF16> r;
+    r.w[0] = src[0];
+    if (!BF16) r.w[BF16 ? 0 : 1] = src[threads];
+    return r;
+}
+
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int W>
@@ -88,251 +215,334 @@ __device__ __forceinline__ float group_sum(float v)
 }
 
 // XB: x is BF16.  V: granules per thread.  LANES: lanes of a row's group in a
-// warp (8 or 32); WIDE: 0, or the largest block the row may belong to.
+// warp (8, 16 or 32); WIDE: 0, or the largest block the row may belong to.
 template <bool XB, int OUT, int V, int LANES, int WIDE>
-__global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads) k_norm_fwd(NormArgs a)
+__global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 : 1) k_norm_fwd(NormArgs a)
 {
+    constexpr int kDepth = depth<XB>(WIDE, V, 1), P = pieces<XB>(), ESZ = XB ? 2 : 4;
+    extern __shared__ uint4 smem_rows[];
     __shared__ float2 sStat[WIDE ? 2 : 1][32];
     pdl_enter();
     const int T = WIDE ? blockDim.x : LANES;
     const int t = WIDE ? threadIdx.x : threadIdx.x % LANES;
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rpb = WIDE ? 1 : kSmallThreads / LANES;           // rows in flight per block
     const int nw = blockDim.x >> 5;
+    const int nt = blockDim.x;
+    const bool tail = a.cols & 7;
 
+    const int step = gridDim.x * rpb;
+    // the groups of a warp leave the loop together (shuffles): wrow is the warp's first row
+    int row = blockIdx.x * rpb + (WIDE ? 0 : threadIdx.x / LANES);
+    int wrow = WIDE ? row : blockIdx.x * rpb + warp * (32 / LANES);
     int valid[V];
-    float gm[V][8], bt[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) valid[v] = max(0, min(8, a.cols - (t + v * T) * 8));
+
+    uint4 *ring = smem_rows + threadIdx.x;                       // [kDepth][V][P][nt]
+    const uint8_t *src = static_cast<const uint8_t *>(a.x) + ((int64_t)row * a.ldx + t * 8) * ESZ;
+    const int64_t src_step = (int64_t)step * a.ldx * ESZ;
+    constexpr int OSZ = OUT == OUT_BF16 ? 2 : OUT == OUT_F32 ? 4 : 1;
+    uint8_t *dst = static_cast<uint8_t *>(a.y) + ((int64_t)row * a.ldy + t * 8) * OSZ;
+    const int64_t dst_step = (int64_t)step * a.ldy * OSZ;
+    int frow = row;                                              // the next row to fetch
+    // granules past the row read as 0 for good; those of rows past the last one are never used
+#pragma unroll
+    for (int i = 0; i < kDepth * V; ++i)
+        if (valid[i % V] == 0)
+#pragma unroll
+            for (int p = 0; p < P; ++p) ring[(i * P + p) * nt] = make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int stage) {
+        if (frow < a.rows) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (valid[v] > 0)
+                    fetch8<XB>(ring + (stage * V + v) * P * nt, nt, src + v * T * 8 * ESZ, valid[v]);
+        }
+        fetch_commit();
+        frow += step;
+        src += src_step;
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+
+    f2 gm[V][4], bt[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int col = (t + v * T) * 8;
-        valid[v] = max(0, min(8, a.cols - col));
-        load_params(a.gamma, a.param_bf16, col, valid[v], 1.0f, gm[v]);
-        load_params(a.beta, a.param_bf16, col, valid[v], 0.0f, bt[v]);
+        load_params(a.gamma, a.param_bf16, (t + v * T) * 8, valid[v], 1.0f, gm[v]);
+        load_params(a.beta, a.param_bf16, (t + v * T) * 8, valid[v], 0.0f, bt[v]);
     }
-    // elements of this warp's (or group's) part of a row
-    float n_w = 0.0f;
+    // elements of a row in this warp's (or group's) part, and in that of warp `lane`
+    float n_w = 0.0f, n_l = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) n_w += (float)valid[v];
+    for (int v = 0; v < V; ++v) {
+        n_w += (float)valid[v];
+        if (WIDE && lane < nw) n_l += (float)max(0, min(256, a.cols - (lane * 32 + v * T) * 8));
+    }
     n_w = group_sum<LANES>(n_w);
-    const float inv_n_w = n_w > 0.0f ? 1.0f / n_w : 0.0f;
+    const float inv_n_w = n_w > 0.0f ? 1.0f / n_w : 0.0f, inv_n_l = n_l > 0.0f ? 1.0f / n_l : 0.0f;
 
     uint32_t bad = 0;
-    int buf = 0;
-    const int64_t step = (int64_t)gridDim.x * rpb;
-    // the groups of a warp leave the loop together (shuffles): wrow is the warp's first row
-    int64_t row = (int64_t)blockIdx.x * rpb + (WIDE ? 0 : threadIdx.x / LANES);
-    int64_t wrow = WIDE ? row : (int64_t)blockIdx.x * rpb + warp * (32 / LANES);
-    Raw8<XB> cur[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        cur[v] = load_raw8<XB>(a.x, row * a.ldx + (t + v * T) * 8, row < a.rows ? valid[v] : 0);
-    for (; wrow < a.rows; wrow += step, row += step) {
+    int buf = 0, stage = 0;
+    for (; wrow < a.rows;) {
         const bool live = row < a.rows;
-        float x[V][8];
+        fetch((stage + kDepth - 1) % kDepth);
+        fetch_wait<kDepth - 1>();
+        f2 x[V][4];
 #pragma unroll
-        for (int v = 0; v < V; ++v) widen8<XB>(cur[v], x[v]);
-        const int64_t nrow = row + step;
-#pragma unroll
-        for (int v = 0; v < V; ++v)                              // the next row is in flight meanwhile
-            cur[v] = load_raw8<XB>(a.x, nrow * a.ldx + (t + v * T) * 8, nrow < a.rows ? valid[v] : 0);
+        for (int v = 0; v < V; ++v) widen8<XB>(fetched8<XB>(ring + (stage * V + v) * P * nt, nt), x[v]);
+        stage = (stage + 1) % kDepth;
 
-        float s = 0.0f;
+        f2 s = 0;                                                // elements past the row read as 0
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) s = add2(s, add2(add2(x[v][0], x[v][1]), add2(x[v][2], x[v][3])));
+        const float sum_w = group_sum<LANES>(sum2(s));
+        float mean = sum_w * inv_n_w, m2 = 0.0f;
+        {
+            const f2 neg = pack2(-mean, -mean);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += x[v][i];            // elements past the row read as 0
-        float mean = group_sum<LANES>(s) * inv_n_w;
-        float m2 = 0.0f;
+            for (int v = 0; v < V; ++v) {
+                f2 d[4], q = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+                for (int i = 0; i < 4; ++i) d[i] = add2(x[v][i], neg);
+                if (tail) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = x[v][i] - mean;
-                m2 += i < valid[v] ? d * d : 0.0f;
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 e = unpack2(d[i]);
+                        d[i] = pack2(2 * i < valid[v] ? e.x : 0.0f, 2 * i + 1 < valid[v] ? e.y : 0.0f);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q = fma2(d[i], d[i], q);
+                m2 += valid[v] > 0 ? sum2(q) : 0.0f;
             }
+        }
         m2 = group_sum<LANES>(m2);
         if (WIDE) {
-            if ((threadIdx.x & 31) == 0) sStat[buf][warp] = make_float2(mean * n_w, m2);
+            if (lane == 0) sStat[buf][warp] = make_float2(sum_w, m2);
             __syncthreads();
-            // lane w holds warp w's part; n_w of another warp follows from its columns
-            const int lane = threadIdx.x & 31;
             const float2 p = lane < nw ? sStat[buf][lane] : make_float2(0.0f, 0.0f);
-            float n = 0.0f;
-            if (lane < nw) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) n += (float)max(0, min(256, a.cols - (lane * 32 + v * T) * 8));
-            }
-            mean = group_sum<32>(p.x) * a.inv_cols;
-            const float d = n > 0.0f ? p.x / n - mean : 0.0f;
-            m2 = group_sum<32>(p.y + n * d * d);
+            mean = warps_sum(p.x, nw) * a.inv_cols;
+            const float d = p.x * inv_n_l - mean;
+            m2 = warps_sum(fmaf(n_l * d, d, p.y), nw);
             buf ^= 1;
         }
-        const float var = m2 * a.inv_cols;
-        const float rstd = __frsqrt_rn(var + a.eps);
+        const float rstd = __frsqrt_rn(fmaf(m2, a.inv_cols, a.eps));
         if (t == 0 && live) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
+        const f2 neg = pack2(-mean, -mean), r2 = pack2(rstd, rstd);
+        float y[V][8];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int col = (t + v * T) * 8;
-            float y[8];
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf((x[v][i] - mean) * rstd, gm[v][i], bt[v][i]);
-            const int n = live ? valid[v] : 0;
-            if (OUT != OUT_F8) {
-                if (n > 0) store8<OUT == OUT_BF16>(a.y, row * a.ldy + col, y, n);
-            } else {
+            for (int i = 0; i < 4; ++i) {
+                const float2 e = unpack2(fma2(mul2(add2(x[v][i], neg), r2), gm[v][i], bt[v][i]));
+                y[v][2 * i] = e.x;
+                y[v][2 * i + 1] = e.y;
+            }
+        if (OUT == OUT_BF16 || OUT == OUT_F32) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i >= n) y[i] = 0.0f;
-                constexpr int W = LANES < 16 ? LANES : 16;       // lanes of a 128-block
-                uint32_t m = amax_bits(y);
+            for (int v = 0; v < V; ++v)
+                if (live && valid[v] > 0)
+                    store8<OUT == OUT_BF16>(dst, v * T * 8, y[v], valid[v]);
+        } else {
+            constexpr int W = LANES < 16 ? LANES : 16;           // lanes of a 128-block
+            float m[V];
+            bool ok = true;
 #pragma unroll
-                for (int o = W / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                if (__any_sync(0xFFFFFFFFu, m >= kInfBits)) {    // rare: map what is not finite, and again
-                    sanitize_all(y, bad);
-                    m = amax_bits(y);
+            for (int v = 0; v < V; ++v) {
+                if (!live || valid[v] < 8) {
 #pragma unroll
-                    for (int o = W / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                    for (int i = 0; i < 8; ++i)
+                        if (!live || i >= valid[v]) y[v][i] = 0.0f;
                 }
-                const float s = scale_or_factor(m, a.fmax, t & 1);
-                const float f = __shfl_sync(0xFFFFFFFFu, s, 0, W);
-                uint32_t lo, hi;
-                if (a.e5m2) {
-                    lo = encode4<true>(y[0], y[1], y[2], y[3], f);
-                    hi = encode4<true>(y[4], y[5], y[6], y[7], f);
-                } else {
-                    lo = encode4<false>(y[0], y[1], y[2], y[3], f);
-                    hi = encode4<false>(y[4], y[5], y[6], y[7], f);
+                m[v] = amax8_nan(y[v]);
+            }
+#pragma unroll
+            for (int o = W / 2; o; o >>= 1)
+#pragma unroll
+                for (int v = 0; v < V; ++v) m[v] = max_nan(m[v], __shfl_xor_sync(0xFFFFFFFFu, m[v], o));
+#pragma unroll
+            for (int v = 0; v < V; ++v) ok = ok && m[v] <= 3.402823466e38f;      // false for NaN too
+            if (!__all_sync(0xFFFFFFFFu, ok)) {                  // rare: map what is not finite, and again
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    sanitize_all(y[v], bad);
+                    m[v] = amax8_nan(y[v]);
+#pragma unroll
+                    for (int o = W / 2; o; o >>= 1) m[v] = max_nan(m[v], __shfl_xor_sync(0xFFFFFFFFu, m[v], o));
                 }
-                if (n > 0) {
-                    store_codes8(static_cast<uint8_t *>(a.y) + row * a.ldy + col, lo, hi, n);
-                }
-                // the block's second lane holds the scale
-                if (live && t % W == 1 && col - 8 < a.cols) a.scale[(int64_t)(col / BLK) * a.lds + row] = s;
+            }
+            // lane 2 v forms the factor of the block of granule v, lane 2 v + 1 its scale
+            const int l = t % W;
+            float mine = m[0];
+#pragma unroll
+            for (int v = 1; v < V; ++v) mine = (l >> 1) == v ? m[v] : mine;
+            const float s8 = scale_or_factor(f_bits(mine), fmt_max(OUT == OUT_E5M2 ? HIF4_E5M2 : HIF4_E4M3), l & 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int col = (t + v * T) * 8;
+                const float f = __shfl_sync(0xFFFFFFFFu, s8, 2 * v, W);
+                const uint32_t lo = encode4<OUT == OUT_E5M2>(y[v][0], y[v][1], y[v][2], y[v][3], f);
+                const uint32_t hi = encode4<OUT == OUT_E5M2>(y[v][4], y[v][5], y[v][6], y[v][7], f);
+                if (live && valid[v] > 0)
+                    store_codes8(dst + v * T * 8, lo, hi, valid[v]);
+                if (live && l == 2 * v + 1 && col - l * 8 < a.cols)
+                    a.scale[(int64_t)(col / BLK) * a.lds + row] = s8;
             }
         }
+        row += step;
+        wrow += step;
+        dst += dst_step;
     }
     if (bad) status_or(a.status, HIF4_FLAG_NONFINITE);
 }
 
 template <bool XB, int V, int LANES, int WIDE>
-__global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads) k_norm_bwd(NormBwdArgs a)
+__global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 ? 2 : 1) k_norm_bwd(NormBwdArgs a)
 {
+    constexpr int kDepth = depth<XB>(WIDE, V, 2), P = pieces<XB>(), ESZ = XB ? 2 : 4;
+    extern __shared__ uint4 smem_rows[];
     __shared__ float2 sSum[WIDE ? 2 : 1][32];
-    __shared__ float sCol[WIDE ? 1 : kSmallThreads * V * 8];     // column sums of the block's row groups
     pdl_enter();
     const int T = WIDE ? blockDim.x : LANES;
     const int t = WIDE ? threadIdx.x : threadIdx.x % LANES;
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rpb = WIDE ? 1 : kSmallThreads / LANES;
     const int nw = blockDim.x >> 5;
+    const int nt = blockDim.x;
 
+    const int step = gridDim.x * rpb;
+    int row = blockIdx.x * rpb + (WIDE ? 0 : threadIdx.x / LANES);
+    int wrow = WIDE ? row : blockIdx.x * rpb + warp * (32 / LANES);
     int valid[V];
-    float gm[V][8], dg[V][8], db[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) valid[v] = max(0, min(8, a.cols - (t + v * T) * 8));
+
+    uint4 *ring = smem_rows + threadIdx.x;                       // [kDepth][x, dy][V][P][nt]
+    const uint8_t *xs = static_cast<const uint8_t *>(a.x) + ((int64_t)row * a.ldx + t * 8) * ESZ;
+    const uint8_t *ds = static_cast<const uint8_t *>(a.dy) + ((int64_t)row * a.lddy + t * 8) * ESZ;
+    const int64_t x_step = (int64_t)step * a.ldx * ESZ, d_step = (int64_t)step * a.lddy * ESZ;
+    uint8_t *dst = static_cast<uint8_t *>(a.dx) + ((int64_t)row * a.lddx + t * 8) * ESZ;
+    const int64_t dst_step = (int64_t)step * a.lddx * ESZ;
+    int frow = row;
+    auto fetch = [&](int stage) {
+        const bool in = frow < a.rows;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int n = in ? valid[v] : 0;
+            fetch8<XB>(ring + (stage * 2 * V + v) * P * nt, nt,
+                       n > 0 ? xs + v * T * 8 * ESZ : static_cast<const uint8_t *>(a.x), n);
+            fetch8<XB>(ring + (stage * 2 * V + V + v) * P * nt, nt,
+                       n > 0 ? ds + v * T * 8 * ESZ : static_cast<const uint8_t *>(a.dy), n);
+        }
+        fetch_commit();
+        if (in) {
+            xs += x_step;
+            ds += d_step;
+        }
+        frow += step;
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+
+    f2 gm[V][4], dg[V][4], db[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int col = (t + v * T) * 8;
-        valid[v] = max(0, min(8, a.cols - col));
-        load_params(a.gamma, a.param_bf16, col, valid[v], 1.0f, gm[v]);
+        load_params(a.gamma, a.param_bf16, (t + v * T) * 8, valid[v], 1.0f, gm[v]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[v][i] = db[v][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) dg[v][i] = db[v][i] = 0;
     }
-    int buf = 0;
-    const int64_t step = (int64_t)gridDim.x * rpb;
-    int64_t row = (int64_t)blockIdx.x * rpb + (WIDE ? 0 : threadIdx.x / LANES);
-    int64_t wrow = WIDE ? row : (int64_t)blockIdx.x * rpb + warp * (32 / LANES);
-    Raw8<XB> cx[V], cd[V];
-    float cmean = 0.0f, crstd = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int n = row < a.rows ? valid[v] : 0;
-        cx[v] = load_raw8<XB>(a.x, row * a.ldx + (t + v * T) * 8, n);
-        cd[v] = load_raw8<XB>(a.dy, row * a.lddy + (t + v * T) * 8, n);
-    }
-    if (row < a.rows) {
-        cmean = a.mean[row];
-        crstd = a.rstd[row];
-    }
-    for (; wrow < a.rows; wrow += step, row += step) {
+    int buf = 0, stage = 0;
+    // Statistics a row ahead.  0 past the last row, where dy reads as 0 too: nothing is added there.
+    float cmean = row < a.rows ? a.mean[row] : 0.0f, crstd = row < a.rows ? a.rstd[row] : 0.0f;
+    for (; wrow < a.rows;) {
         const bool live = row < a.rows;
         const float mean = cmean, rstd = crstd;
-        float s1 = 0.0f, s2 = 0.0f;
-        float xh[V][8], d[V][8];
+        const int nrow = row + step;
+        cmean = nrow < a.rows ? a.mean[nrow] : 0.0f;
+        crstd = nrow < a.rows ? a.rstd[nrow] : 0.0f;
+        fetch((stage + kDepth - 1) % kDepth);
+        fetch_wait<kDepth - 1>();
+        f2 xh[V][4], w[V][4], s1 = 0, s2 = 0;
+        const f2 neg = pack2(-mean, -mean), r2 = pack2(rstd, rstd);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            widen8<XB>(cx[v], xh[v]);
-            widen8<XB>(cd[v], d[v]);                             // 0 past the row and for rows past the end
-        }
-        const int64_t nrow = row + step;
+            f2 d[4];
+            widen8<XB>(fetched8<XB>(ring + (stage * 2 * V + v) * P * nt, nt), xh[v]);
+            widen8<XB>(fetched8<XB>(ring + (stage * 2 * V + V + v) * P * nt, nt), d);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int n = nrow < a.rows ? valid[v] : 0;
-            cx[v] = load_raw8<XB>(a.x, nrow * a.ldx + (t + v * T) * 8, n);
-            cd[v] = load_raw8<XB>(a.dy, nrow * a.lddy + (t + v * T) * 8, n);
-        }
-        if (nrow < a.rows) {
-            cmean = a.mean[nrow];
-            crstd = a.rstd[nrow];
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int n = live ? valid[v] : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                xh[v][i] = i < n ? (xh[v][i] - mean) * rstd : 0.0f;
-                dg[v][i] = fmaf(d[v][i], xh[v][i], dg[v][i]);
-                db[v][i] += d[v][i];
-                d[v][i] *= gm[v][i];
-                s1 += d[v][i];
-                s2 = fmaf(d[v][i], xh[v][i], s2);
+            for (int i = 0; i < 4; ++i) {
+                xh[v][i] = mul2(add2(xh[v][i], neg), r2);
+                dg[v][i] = fma2(d[i], xh[v][i], dg[v][i]);
+                db[v][i] = add2(db[v][i], d[i]);
+                w[v][i] = mul2(d[i], gm[v][i]);
+                s1 = add2(s1, w[v][i]);
+                s2 = fma2(w[v][i], xh[v][i], s2);
             }
         }
-        s1 = group_sum<LANES>(s1);
-        s2 = group_sum<LANES>(s2);
+        stage = (stage + 1) % kDepth;
+        float t1 = group_sum<LANES>(sum2(s1)), t2 = group_sum<LANES>(sum2(s2));
         if (WIDE) {
-            if ((threadIdx.x & 31) == 0) sSum[buf][warp] = make_float2(s1, s2);
+            if (lane == 0) sSum[buf][warp] = make_float2(t1, t2);
             __syncthreads();
-            const int lane = threadIdx.x & 31;
             const float2 p = lane < nw ? sSum[buf][lane] : make_float2(0.0f, 0.0f);
-            s1 = group_sum<32>(p.x);
-            s2 = group_sum<32>(p.y);
+            t1 = warps_sum(p.x, nw);
+            t2 = warps_sum(p.y, nw);
             buf ^= 1;
         }
-        const float c1 = s1 * a.inv_cols, c2 = s2 * a.inv_cols;
         if (a.dx) {
+            const float c1 = t1 * a.inv_cols, c2 = t2 * a.inv_cols;
+            const f2 n1 = pack2(-c1, -c1), n2 = pack2(-c2, -c2);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = rstd * (d[v][i] - c1 - xh[v][i] * c2);
-                if (live && valid[v] > 0) store8<XB>(a.dx, row * a.lddx + (t + v * T) * 8, o, valid[v]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = unpack2(mul2(fma2(xh[v][i], n2, add2(w[v][i], n1)), r2));
+                    o[2 * i] = e.x;
+                    o[2 * i + 1] = e.y;
+                }
+                if (live && valid[v] > 0) store8<XB>(dst, v * T * 8, o, valid[v]);
             }
         }
+        row += step;
+        wrow += step;
+        dst += dst_step;
     }
     if (!a.part) return;
-    float *pg = a.part + (int64_t)blockIdx.x * 2 * a.cols, *pb = pg + a.cols;
+    const int pitch = (a.cols + 7) & ~7;
+    float *pg = a.part + (int64_t)blockIdx.x * 2 * pitch, *pb = pg + pitch;
     if (WIDE) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
+            if (valid[v] > 0) {                                  // whole granules: the pitch has room
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < valid[v]) {
-                    pg[(t + v * T) * 8 + i] = dg[v][i];
-                    pb[(t + v * T) * 8 + i] = db[v][i];
+                for (int i = 0; i < 2; ++i) {
+                    const float2 g0 = unpack2(dg[v][2 * i]), g1 = unpack2(dg[v][2 * i + 1]);
+                    const float2 b0 = unpack2(db[v][2 * i]), b1 = unpack2(db[v][2 * i + 1]);
+                    reinterpret_cast<float4 *>(pg + (t + v * T) * 8)[i] = make_float4(g0.x, g0.y, g1.x, g1.y);
+                    reinterpret_cast<float4 *>(pb + (t + v * T) * 8)[i] = make_float4(b0.x, b0.y, b1.x, b1.y);
                 }
+            }
     } else {
-        // the block's row groups, added in order: group g's sums lie at g * (LANES V 8)
+        // The block's row groups, added in order: group g's sums lie at g * W in the memory of the rows,
+        // of which no copy is in flight any more.
         constexpr int W = LANES * V * 8;
+        float *sCol = reinterpret_cast<float *>(smem_rows);
         const int g = threadIdx.x / LANES;
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
-            if (pass) __syncthreads();
+            __syncthreads();
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sCol[g * W + (t + v * LANES) * 8 + i] = pass ? db[v][i] : dg[v][i];
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float2 *>(sCol + g * W + (t + v * LANES) * 8 + 2 * i) =
+                        unpack2(pass ? db[v][i] : dg[v][i]);
             __syncthreads();
             for (int c = threadIdx.x; c < a.cols; c += kSmallThreads) {
                 float s = 0.0f;
@@ -350,79 +560,94 @@ __global__ void __launch_bounds__(1024) k_norm_bwd_join(const float *part, int p
 {
     __shared__ float s[32][33];
     pdl_enter();
-    const int c = blockIdx.x * 32 + threadIdx.x;                 // over 2 x cols: dgamma, then dbeta
+    const int pitch = (cols + 7) & ~7;
+    const int c = blockIdx.x * 32 + threadIdx.x;                 // over 2 x pitch: dgamma, then dbeta
     float v = 0.0f;
-    if (c < 2 * cols)
-        for (int p = threadIdx.y; p < parts; p += 32) v += part[(int64_t)p * 2 * cols + c];
+    if (c < 2 * pitch) {
+#pragma unroll 4
+        for (int p = threadIdx.y; p < parts; p += 32) v += part[(int64_t)p * 2 * pitch + c];
+    }
     s[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     v = s[threadIdx.x][threadIdx.y];                             // lane = part, warp = column
     v = group_sum<32>(v);
     const int co = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && co < 2 * cols) {
+    if (threadIdx.x == 0) {
         if (co < cols) {
             if (dgamma) dgamma[co] = v;
-        } else if (dbeta) {
-            dbeta[co - cols] = v;
+        } else if (dbeta && co >= pitch && co - pitch < cols) {
+            dbeta[co - pitch] = v;
         }
     }
 }
 
-// Threads of a row's group and granules per thread.  8 lanes up to 64 columns,
-// a warp up to 1024, then a block.
+// Threads of a row's group and granules per thread: 8, 16 or 32 lanes of a warp
+// up to 1024 columns, a block beyond.
 struct Shape {
     int lanes, v, threads, wide;
 };
 
-Shape shape_of(int64_t cols)
+Shape shape_of(int64_t cols, int wide_v)
 {
     const int g = (int)((cols + 7) / 8);
     if (g <= 8) return Shape{8, 1, kSmallThreads, 0};
+    if (g <= 16) return Shape{16, 1, kSmallThreads, 0};
     if (g <= 32) return Shape{32, 1, kSmallThreads, 0};
     if (g <= 64) return Shape{32, 2, kSmallThreads, 0};
     if (g <= 128) return Shape{32, 4, kSmallThreads, 0};
-    return Shape{32, 2, (g + 63) / 64 * 32, g <= 1024 ? 512 : 1024};
+    const int threads = (g + 32 * wide_v - 1) / (32 * wide_v) * 32;
+    return Shape{32, wide_v, threads, threads <= 640 / wide_v ? 640 / wide_v : threads <= 512 ? 512 : 1024};
+}
+
+// Blocks of a persistent launch over `rows`, and its dynamic shared memory.
+template <typename A>
+hif4_status grid_of(void (*k)(A), const Shape &sh, int rows, size_t smem, int64_t &grid)
+{
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_failed(e);
+    const int rpb = sh.wide ? 1 : kSmallThreads / sh.lanes;
+    grid = ((int64_t)rows + rpb - 1) / rpb;
+    const int64_t most = (int64_t)sm_count() * blocks_per_sm(reinterpret_cast<const void *>(k), sh.threads, smem);
+    if (grid > most) grid = most;
+    return HIF4_OK;
 }
 
 template <bool XB, int OUT>
 hif4_status launch_fwd(const NormArgs &a, cudaStream_t s)
 {
-    const Shape sh = shape_of(a.cols);
-    void (*k)(NormArgs);
-    if (sh.wide)
-        k = sh.wide == 512 ? k_norm_fwd<XB, OUT, 2, 32, 512> : k_norm_fwd<XB, OUT, 2, 32, 1024>;
-    else if (sh.lanes == 8)
-        k = k_norm_fwd<XB, OUT, 1, 8, 0>;
-    else
-        k = sh.v == 1 ? k_norm_fwd<XB, OUT, 1, 32, 0>
-                      : sh.v == 2 ? k_norm_fwd<XB, OUT, 2, 32, 0> : k_norm_fwd<XB, OUT, 4, 32, 0>;
-    const int rpb = sh.wide ? 1 : kSmallThreads / sh.lanes;
-    int64_t grid = ((int64_t)a.rows + rpb - 1) / rpb;
-    const int64_t most = (int64_t)sm_count() * blocks_per_sm(reinterpret_cast<const void *>(k), sh.threads, 0);
-    if (grid > most) grid = most;
-    return launch_pdl(k, dim3((unsigned)grid), dim3((unsigned)sh.threads), 0, s, a);
+    const Shape sh = shape_of(a.cols, 4);
+    void (*k)(NormArgs) = sh.wide == 160 ? k_norm_fwd<XB, OUT, 4, 32, 160>
+                          : sh.wide ? k_norm_fwd<XB, OUT, 4, 32, 512>
+                          : sh.lanes == 8 ? k_norm_fwd<XB, OUT, 1, 8, 0>
+                          : sh.lanes == 16 ? k_norm_fwd<XB, OUT, 1, 16, 0>
+                          : sh.v == 1 ? k_norm_fwd<XB, OUT, 1, 32, 0>
+                          : sh.v == 2 ? k_norm_fwd<XB, OUT, 2, 32, 0> : k_norm_fwd<XB, OUT, 4, 32, 0>;
+    const size_t smem = (size_t)depth<XB>(sh.wide, sh.v, 1) * sh.v * pieces<XB>() * sh.threads * 16;
+    int64_t grid;
+    const hif4_status st = grid_of(k, sh, a.rows, smem, grid);
+    if (st != HIF4_OK) return st;
+    return launch_pdl(k, dim3((unsigned)grid), dim3((unsigned)sh.threads), smem, s, a);
 }
 
 template <bool XB>
 hif4_status launch_bwd(const NormBwdArgs &a, float *dgamma, float *dbeta, cudaStream_t s)
 {
-    const Shape sh = shape_of(a.cols);
-    void (*k)(NormBwdArgs);
-    if (sh.wide)
-        k = sh.wide == 512 ? k_norm_bwd<XB, 2, 32, 512> : k_norm_bwd<XB, 2, 32, 1024>;
-    else if (sh.lanes == 8)
-        k = k_norm_bwd<XB, 1, 8, 0>;
-    else
-        k = sh.v == 1 ? k_norm_bwd<XB, 1, 32, 0>
-                      : sh.v == 2 ? k_norm_bwd<XB, 2, 32, 0> : k_norm_bwd<XB, 4, 32, 0>;
-    const int rpb = sh.wide ? 1 : kSmallThreads / sh.lanes;
-    int64_t grid = ((int64_t)a.rows + rpb - 1) / rpb;
-    const int64_t most = (int64_t)sm_count() * blocks_per_sm(reinterpret_cast<const void *>(k), sh.threads, 0);
-    if (grid > most) grid = most;
+    const Shape sh = shape_of(a.cols, 2);
+    void (*k)(NormBwdArgs) = sh.wide == 320 ? k_norm_bwd<XB, 2, 32, 320>
+                             : sh.wide == 512 ? k_norm_bwd<XB, 2, 32, 512>
+                             : sh.wide ? k_norm_bwd<XB, 2, 32, 1024>
+                             : sh.lanes == 8 ? k_norm_bwd<XB, 1, 8, 0>
+                             : sh.lanes == 16 ? k_norm_bwd<XB, 1, 16, 0>
+                             : sh.v == 1 ? k_norm_bwd<XB, 1, 32, 0>
+                             : sh.v == 2 ? k_norm_bwd<XB, 2, 32, 0> : k_norm_bwd<XB, 4, 32, 0>;
+    const size_t smem = (size_t)depth<XB>(sh.wide, sh.v, 2) * 2 * sh.v * pieces<XB>() * sh.threads * 16;
+    int64_t grid;
+    hif4_status st = grid_of(k, sh, a.rows, smem, grid);
+    if (st != HIF4_OK) return st;
     if (grid > kMaxPartials) grid = kMaxPartials;
-    hif4_status st = launch_pdl(k, dim3((unsigned)grid), dim3((unsigned)sh.threads), 0, s, a);
+    st = launch_pdl(k, dim3((unsigned)grid), dim3((unsigned)sh.threads), smem, s, a);
     if (st != HIF4_OK || !a.part) return st;
-    return launch_pdl(k_norm_bwd_join, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(32, 32), 0, s, a.part,
+    return launch_pdl(k_norm_bwd_join, dim3((unsigned)((2 * ((a.cols + 7) & ~7) + 31) / 32)), dim3(32, 32), 0, s, a.part,
                       (int)grid, a.cols, dgamma, dbeta);
 }
 
@@ -439,7 +664,7 @@ hif4_status fwd_args(NormArgs &a, const void *x, hif4_dtype dtype, int64_t rows,
     if ((gamma && !aligned_to(gamma, elem(param))) || (beta && !aligned_to(beta, elem(param))) ||
         !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return HIF4_ERR_ALIGNMENT;
-    if (cols > kMaxCols || rows > INT32_MAX) return HIF4_ERR_UNSUPPORTED;
+    if (cols > kMaxCols || rows > kMaxRows) return HIF4_ERR_UNSUPPORTED;
     a.x = x;
     a.ldx = ldx;
     a.gamma = gamma;
@@ -499,18 +724,18 @@ extern "C" hif4_status hif4_layer_norm_f8(const void *x, hif4_dtype dtype, int64
     a.ldy = ldq;
     a.scale = scale;
     a.lds = lds;
-    a.fmax = f8::fmt_max(fmt);
-    a.e5m2 = fmt == HIF4_E5M2;
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == HIF4_BF16 ? launch_fwd<true, OUT_F8>(a, s) : launch_fwd<false, OUT_F8>(a, s);
+    if (fmt == HIF4_E5M2)
+        return dtype == HIF4_BF16 ? launch_fwd<true, OUT_E5M2>(a, s) : launch_fwd<false, OUT_E5M2>(a, s);
+    return dtype == HIF4_BF16 ? launch_fwd<true, OUT_E4M3>(a, s) : launch_fwd<false, OUT_E4M3>(a, s);
 }
 
 extern "C" size_t hif4_layer_norm_backward_workspace(int64_t rows, int64_t cols)
 {
     if (rows <= 0 || cols <= 0 || cols > kMaxCols) return 0;
     const int64_t n = rows < kMaxPartials ? rows : kMaxPartials;
-    return (size_t)n * 2 * (size_t)cols * sizeof(float);
+    return (size_t)n * 2 * (size_t)((cols + 7) & ~(int64_t)7) * sizeof(float);
 }
 
 extern "C" hif4_status hif4_layer_norm_backward(const void *dy, int64_t lddy, const void *x, hif4_dtype dtype,
@@ -521,7 +746,7 @@ extern "C" hif4_status hif4_layer_norm_backward(const void *dy, int64_t lddy, co
 {
     if (rows < 0 || cols < 0 || !valid_dtype(dtype) || !valid_dtype(param_dtype)) return HIF4_ERR_INVALID_ARG;
     if (cols == 0) return HIF4_OK;
-    if (cols > kMaxCols || rows > INT32_MAX) return HIF4_ERR_UNSUPPORTED;
+    if (cols > kMaxCols || rows > kMaxRows) return HIF4_ERR_UNSUPPORTED;
     if (!aligned_to(dgamma, 4) || !aligned_to(dbeta, 4)) return HIF4_ERR_ALIGNMENT;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows == 0) {                                             // sums over no rows
