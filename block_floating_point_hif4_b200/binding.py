@@ -100,6 +100,8 @@ class Hif4Error(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libhif4.so (built in-tree by ``build.py``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -459,9 +461,15 @@ def ptq_state_unpack(record: bytes, device=None):
 
 
 # ------------------------------------------------- block-scaled FP8, layer norm
+#
+# These calls are short enough for their marshalling to count: pointers are
+# passed as integers, a padded allocation is only sliced where it has padding,
+# and no context is entered where device and stream are the current ones.
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 _F8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+_SCALE = {torch.float32: F32}
+_BIAS = {torch.bfloat16: BF16}
 
 
 def _cdiv(n, m):
@@ -474,51 +482,71 @@ def _need(ok, message):
 
 
 def _matrix(t, name, dtypes, shape=None):
-    """Checks a 2-D CUDA tensor whose rows are contiguous."""
-    _dev(t, name)
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "%s must be 2-D with contiguous rows" % name)
-    _need(t.dtype in dtypes, "%s has dtype %s" % (name, t.dtype))
-    _need(shape is None or tuple(t.shape) == tuple(shape), "%s must be %s, is %s" % (name, shape, tuple(t.shape)))
-    return t
+    """Checks a 2-D CUDA tensor whose rows are contiguous -> (rows, cols, leading dimension).  The leading
+    dimension of a single row, which no address depends on, is rounded up to a multiple of 16."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in dtypes:
+        raise ValueError("%s has dtype %s" % (name, t.dtype))
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError("%s must be 2-D" % name)
+    if shape is not None and size != shape:
+        raise ValueError("%s must be %s, is %s" % (name, tuple(shape), tuple(size)))
+    rows, cols = size
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return rows, cols, (ld if rows > 1 else (cols + 15) // 16 * 16)
 
 
 def _vector(t, name, dtypes, n):
-    if t is not None:
-        _dev(t, name)
-        _need(t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1),
-              "%s must be a contiguous vector of %d elements" % (name, n))
-        _need(t.dtype in dtypes, "%s has dtype %s" % (name, t.dtype))
-    return t
+    """Checks an optional contiguous vector -> its address or None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in dtypes:
+        raise ValueError("%s has dtype %s" % (name, t.dtype))
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector of %d elements" % (name, n))
+    return t.data_ptr()
 
 
-def _ld(t, multiple):
-    """Leading dimension; that of a single row, which no address depends on, is rounded up."""
-    return t.stride(0) if t.shape[0] > 1 else _cdiv(t.shape[1], multiple) * multiple
+def _status(t):
+    if t is None:
+        return None
+    if not t.is_cuda or t.element_size() != 4 or t.numel() < 1:
+        raise ValueError("status must be a 32-bit word on the GPU")
+    return t.data_ptr()
 
 
 def _padded(rows, cols, dtype, multiple, device):
     """rows x cols whose leading dimension is a multiple of `multiple` elements."""
-    return torch.empty(rows, _cdiv(cols, multiple) * multiple, dtype=dtype, device=device)[:, :cols]
+    pad = -cols % multiple
+    t = torch.empty(rows, cols + pad, dtype=dtype, device=device)
+    return t[:, :cols] if pad else t
 
 
 @contextlib.contextmanager
 def _switched(device, stream):
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield stream
+        yield stream.cuda_stream
 
 
 def _place(stream, *tensors):
     """Context of a call: its tensors' device current, `stream` (default: that
     device's current stream) current, so that what the call allocates belongs
-    to the stream it runs on.  Yields the stream."""
+    to the stream it runs on.  Yields the stream's handle."""
     dev = tensors[0].device
     for t in tensors:
-        _need(t is None or t.device == dev, "tensors of one call must be on one device")
-    _need(stream is None or stream.device == dev, "the stream is on another device than the tensors")
+        if t is not None and t.device != dev:
+            raise ValueError("tensors of one call must be on one device")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
         if dev.index == torch.cuda.current_device():
-            return contextlib.nullcontext(stream)
+            return contextlib.nullcontext(torch.cuda.current_stream(dev).cuda_stream)
+        stream = torch.cuda.current_stream(dev)
+    _need(stream.device == dev, "the stream is on another device than the tensors")
     return _switched(dev, stream)
 
 
@@ -531,31 +559,30 @@ def quantize_f8(x: torch.Tensor, fmt=torch.float8_e4m3fn, *, block_rows: int = 1
     [ceil(cols/128), rows] for block_rows 1 and [ceil(rows/128),
     ceil(cols/128)] for 128; scale_t likewise for the transposed matrix.
     `out` is a tuple of those tensors to write into."""
-    _matrix(x, "x", _DTYPE)
+    rows, cols, ldx = _matrix(x, "x", _DTYPE)
     _need(fmt in _F8, "fmt must be torch.float8_e4m3fn or torch.float8_e5m2")
     _need(block_rows in (1, 128), "block_rows must be 1 or 128")
     _need(layout in ("rows", "cols", "both"), "layout must be rows, cols or both")
-    rows, cols = x.shape
-    want = {"rows": (1,), "cols": (0,), "both": (1, 0)}[layout]
     sizes = []
-    for direct in want:
-        r, c = (rows, cols) if direct else (cols, rows)
+    for r, c in ((rows, cols),) * (layout != "cols") + ((cols, rows),) * (layout != "rows"):
         sizes += [(r, c), (_cdiv(c, 128), r) if block_rows == 1 else (_cdiv(r, 128), _cdiv(c, 128))]
-    given = tuple(out) if out is not None else ()
-    with _place(stream, x, status, *given) as s:
+    f8 = {fmt: _F8[fmt]}
+    with _place(stream, x, status, *(out if out is not None else ())) as s:
         if out is None:
-            out = tuple(_padded(r, c, torch.float32 if i & 1 else fmt, 4 if i & 1 else 16, x.device)
-                        for i, (r, c) in enumerate(sizes))
+            dev = x.device
+            out = tuple([_padded(r, c, torch.float32, 4, dev) if i & 1 else _padded(r, c, fmt, 16, dev)
+                         for i, (r, c) in enumerate(sizes)])
         _need(len(out) == len(sizes), "out must hold %d tensors" % len(sizes))
-        for i, (t, size) in enumerate(zip(out, sizes)):
-            _matrix(t, "out[%d]" % i, (torch.float32,) if i & 1 else (fmt,), size)
-        q, sc = (out[0], out[1]) if want[0] else (None, None)
-        qt, sct = (out[-2], out[-1]) if not want[-1] else (None, None)
+        args = []
+        for i, size in enumerate(sizes):
+            ld = _matrix(out[i], "out[%d]" % i, _SCALE if i & 1 else f8, size)[2]
+            args += [out[i].data_ptr(), ld]
+        if layout == "rows":
+            args += [None, 0, None, 0]
+        elif layout == "cols":
+            args = [None, 0, None, 0] + args
         _check("hif4_quantize_f8", lib().hif4_quantize_f8(
-            _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 16), _F8[fmt], block_rows, _ptr(q),
-            0 if q is None else _ld(q, 16), _ptr(sc), 0 if sc is None else _ld(sc, 4), _ptr(qt),
-            0 if qt is None else _ld(qt, 16), _ptr(sct), 0 if sct is None else _ld(sct, 4), _ptr(status),
-            ctypes.c_void_p(s.cuda_stream)))
+            x.data_ptr(), _DTYPE[x.dtype], rows, cols, ldx, _F8[fmt], block_rows, *args, _status(status), s))
     return out
 
 
@@ -565,61 +592,51 @@ def gemm_f8_block(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.
     """y = (a, sa) · (b, sb)ᵀ + bias for FP8 operands with a scale per block of
     128 along K: a [M, K] with 1 x 128 blocks, b [N, K] with 128 x 128 blocks
     (b_block_rows 128) or 1 x 128 blocks (1), as quantize_f8 leaves them."""
-    _matrix(a, "a", _F8)
-    M, K = a.shape
-    _matrix(b, "b", _F8)
-    N = b.shape[0]
-    _need(b.shape[1] == K, "a and b must have the same number of columns")
+    M, K, lda = _matrix(a, "a", _F8)
+    N, Kb, ldb = _matrix(b, "b", _F8)
+    _need(Kb == K, "a and b must have the same number of columns")
     _need(b_block_rows in (1, 128), "b_block_rows must be 1 or 128")
     units = _cdiv(K, 128)
-    _matrix(sa, "sa", (torch.float32,), (units, M))
-    _matrix(sb, "sb", (torch.float32,), (units, N) if b_block_rows == 1 else (_cdiv(N, 128), units))
-    _vector(bias, "bias", (torch.bfloat16,), N)
+    ldsa = _matrix(sa, "sa", _SCALE, (units, M))[2]
+    ldsb = _matrix(sb, "sb", _SCALE, (units, N) if b_block_rows == 1 else (_cdiv(N, 128), units))[2]
+    pbias = _vector(bias, "bias", _BIAS, N)
     with _place(stream, a, sa, b, sb, bias, out, status) as s:
         if out is None:
-            out = (_padded(M, N, torch.float32, 4, a.device) if out_f32 else
-                   _padded(M, N, torch.bfloat16, 8, a.device))
-        _matrix(out, "out", _DTYPE, (M, N))
-        flags = LINEAR_OUT_F32 if out.dtype == torch.float32 else 0
+            out = _padded(M, N, torch.float32, 4, a.device) if out_f32 else _padded(M, N, torch.bfloat16, 8, a.device)
+        ldy = _matrix(out, "out", _DTYPE, (M, N))[2]
         _check("hif4_gemm_f8_block", lib().hif4_gemm_f8_block(
-            _ptr(a), _F8[a.dtype], M, K, _ld(a, 16), _ptr(sa), _ld(sa, 4), _ptr(b), _F8[b.dtype], N, _ld(b, 16),
-            _ptr(sb), _ld(sb, 4), b_block_rows, _ptr(bias), _ptr(out), _ld(out, 8), flags, _ptr(status),
-            ctypes.c_void_p(s.cuda_stream)))
+            a.data_ptr(), _F8[a.dtype], M, K, lda, sa.data_ptr(), ldsa, b.data_ptr(), _F8[b.dtype], N, ldb,
+            sb.data_ptr(), ldsb, b_block_rows, pbias, out.data_ptr(), ldy,
+            LINEAR_OUT_F32 if out.dtype == torch.float32 else 0, _status(status), s))
     return out
 
 
 def _norm_params(gamma, beta, cols):
-    _vector(gamma, "gamma", _DTYPE, cols)
-    _vector(beta, "beta", _DTYPE, cols)
-    given = [p for p in (gamma, beta) if p is not None]
-    _need(len({p.dtype for p in given}) <= 1, "gamma and beta must have the same dtype")
-    return _DTYPE[given[0].dtype] if given else F32
-
-
-def _norm_stats(rows, save_stats, device):
-    if not save_stats:
-        return None, None
-    return (torch.empty(rows, dtype=torch.float32, device=device),
-            torch.empty(rows, dtype=torch.float32, device=device))
+    """-> (gamma's address, beta's, their dtype)."""
+    pg, pb = _vector(gamma, "gamma", _DTYPE, cols), _vector(beta, "beta", _DTYPE, cols)
+    _need(gamma is None or beta is None or gamma.dtype == beta.dtype, "gamma and beta must have the same dtype")
+    given = gamma if gamma is not None else beta
+    return pg, pb, F32 if given is None else _DTYPE[given.dtype]
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
                eps: float = 1e-6, *, out=None, out_dtype=None, save_stats: bool = False, stream=None):
     """Layer norm of the rows of x -> y, or (y, mean, rstd) with save_stats;
     y has out_dtype (default: x's)."""
-    _matrix(x, "x", _DTYPE)
-    rows, cols = x.shape
-    pdt = _norm_params(gamma, beta, cols)
+    rows, cols, ldx = _matrix(x, "x", _DTYPE)
+    pg, pb, pdt = _norm_params(gamma, beta, cols)
     with _place(stream, x, gamma, beta, out) as s:
         if out is None:
             dt = out_dtype if out_dtype is not None else x.dtype
             _need(dt in _DTYPE, "out_dtype must be float32 or bfloat16")
             out = _padded(rows, cols, dt, 8, x.device)
-        _matrix(out, "out", _DTYPE, (rows, cols))
-        mean, rstd = _norm_stats(rows, save_stats, x.device)
+        ldy = _matrix(out, "out", _DTYPE, (rows, cols))[2]
+        mean = rstd = None
+        if save_stats:
+            mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=x.device).unbind(0)
         _check("hif4_layer_norm", lib().hif4_layer_norm(
-            _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 8), _ptr(gamma), _ptr(beta), pdt, float(eps), _ptr(out),
-            _DTYPE[out.dtype], _ld(out, 8), _ptr(mean), _ptr(rstd), ctypes.c_void_p(s.cuda_stream)))
+            x.data_ptr(), _DTYPE[x.dtype], rows, cols, ldx, pg, pb, pdt, eps, out.data_ptr(), _DTYPE[out.dtype], ldy,
+            mean.data_ptr() if save_stats else None, rstd.data_ptr() if save_stats else None, s))
     return (out, mean, rstd) if save_stats else out
 
 
@@ -628,23 +645,23 @@ def layer_norm_f8(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torc
                   stream=None):
     """layer_norm in FP32 followed by quantize_f8 in 1 x 128 blocks, in one
     pass -> (q, scale), or (q, scale, mean, rstd) with save_stats."""
-    _matrix(x, "x", _DTYPE)
+    rows, cols, ldx = _matrix(x, "x", _DTYPE)
     _need(fmt in _F8, "fmt must be torch.float8_e4m3fn or torch.float8_e5m2")
-    rows, cols = x.shape
-    pdt = _norm_params(gamma, beta, cols)
-    given = tuple(out) if out is not None else ()
-    with _place(stream, x, gamma, beta, status, *given) as s:
+    pg, pb, pdt = _norm_params(gamma, beta, cols)
+    units = _cdiv(cols, 128)
+    with _place(stream, x, gamma, beta, status, *(out if out is not None else ())) as s:
         if out is None:
-            out = (_padded(rows, cols, fmt, 16, x.device),
-                   _padded(_cdiv(cols, 128), rows, torch.float32, 4, x.device))
+            out = _padded(rows, cols, fmt, 16, x.device), _padded(units, rows, torch.float32, 4, x.device)
         q, sc = out
-        _matrix(q, "out[0]", (fmt,), (rows, cols))
-        _matrix(sc, "out[1]", (torch.float32,), (_cdiv(cols, 128), rows))
-        mean, rstd = _norm_stats(rows, save_stats, x.device)
+        ldq = _matrix(q, "out[0]", {fmt: 0}, (rows, cols))[2]
+        lds = _matrix(sc, "out[1]", _SCALE, (units, rows))[2]
+        mean = rstd = None
+        if save_stats:
+            mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=x.device).unbind(0)
         _check("hif4_layer_norm_f8", lib().hif4_layer_norm_f8(
-            _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 8), _ptr(gamma), _ptr(beta), pdt, float(eps), _F8[fmt],
-            _ptr(q), _ld(q, 16), _ptr(sc), _ld(sc, 4), _ptr(mean), _ptr(rstd), _ptr(status),
-            ctypes.c_void_p(s.cuda_stream)))
+            x.data_ptr(), _DTYPE[x.dtype], rows, cols, ldx, pg, pb, pdt, eps, _F8[fmt], q.data_ptr(), ldq,
+            sc.data_ptr(), lds, mean.data_ptr() if save_stats else None, rstd.data_ptr() if save_stats else None,
+            _status(status), s))
     return (q, sc, mean, rstd) if save_stats else (q, sc)
 
 
@@ -657,31 +674,26 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     """Gradients of layer_norm -> (dx, dgamma, dbeta), from the statistics it
     saved.  dx has x's dtype, dgamma and dbeta are FP32.  `out` is a tuple of
     the three, None in the place of one that is not wanted."""
-    _matrix(x, "x", _DTYPE)
-    rows, cols = x.shape
-    _matrix(dy, "dy", (x.dtype,), (rows, cols))
-    _vector(mean, "mean", (torch.float32,), rows)
-    _vector(rstd, "rstd", (torch.float32,), rows)
+    rows, cols, ldx = _matrix(x, "x", _DTYPE)
+    lddy = _matrix(dy, "dy", {x.dtype: 0}, (rows, cols))[2]
     _need(mean is not None and rstd is not None, "mean and rstd are needed")
-    pdt = _norm_params(gamma, None, cols)
-    given = tuple(out) if out is not None else ()
-    with _place(stream, x, dy, mean, rstd, gamma, workspace, *given) as s:
+    pmean, prstd = _vector(mean, "mean", _SCALE, rows), _vector(rstd, "rstd", _SCALE, rows)
+    pg, _, pdt = _norm_params(gamma, None, cols)
+    with _place(stream, x, dy, mean, rstd, gamma, workspace, *(out if out is not None else ())) as s:
         if out is None:
             out = (_padded(rows, cols, x.dtype, 8, x.device),
-                   torch.empty(cols, dtype=torch.float32, device=x.device),
-                   torch.empty(cols, dtype=torch.float32, device=x.device))
+                   *torch.empty(2, cols, dtype=torch.float32, device=x.device).unbind(0))
         dx, dgamma, dbeta = out
-        if dx is not None:
-            _matrix(dx, "out[0]", (x.dtype,), (rows, cols))
-        _vector(dgamma, "out[1]", (torch.float32,), cols)
-        _vector(dbeta, "out[2]", (torch.float32,), cols)
-        if workspace is None:
+        lddx = 0 if dx is None else _matrix(dx, "out[0]", {x.dtype: 0}, (rows, cols))[2]
+        pdg, pdb = _vector(dgamma, "out[1]", _SCALE, cols), _vector(dbeta, "out[2]", _SCALE, cols)
+        if workspace is None and (dgamma is not None or dbeta is not None):
             need = layer_norm_backward_workspace(rows, cols)
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        pws, nws = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size())
         _check("hif4_layer_norm_backward", lib().hif4_layer_norm_backward(
-            _ptr(dy), _ld(dy, 8), _ptr(x), _DTYPE[x.dtype], rows, cols, _ld(x, 8), _ptr(mean), _ptr(rstd),
-            _ptr(gamma), pdt, _ptr(dx), 0 if dx is None else _ld(dx, 8), _ptr(dgamma), _ptr(dbeta),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream)))
+            dy.data_ptr(), lddy, x.data_ptr(), _DTYPE[x.dtype], rows, cols, ldx, pmean, prstd, pg, pdt,
+            None if dx is None else dx.data_ptr(), lddx, pdg, pdb, pws, nws, s))
     return dx, dgamma, dbeta
 
 

@@ -147,6 +147,36 @@ int blocks_per_sm(const void *kernel, int threads, size_t dyn_smem)
     return b;
 }
 
+hif4_status allow_smem(const void *kernel, size_t bytes)
+{
+    if (bytes <= 48 * 1024) return HIF4_OK;
+    struct Entry {
+        const void *kernel;
+        int dev;
+        size_t bytes;
+    };
+    static Entry table[256];
+    static int used = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lk(g_mu);
+    Entry *e = nullptr;
+    for (int i = 0; i < used; ++i)
+        if (table[i].kernel == kernel && table[i].dev == dev) e = &table[i];
+    if (e && e->bytes >= bytes) return HIF4_OK;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        return cuda_failed(err);
+    }
+    if (e)
+        e->bytes = bytes;
+    else if (used < 256)
+        table[used++] = Entry{kernel, dev, bytes};
+    return HIF4_OK;
+}
+
 } // namespace hif4
 
 extern "C" hif4_status hif4_get_status(const uint32_t *status_word, hif4_stream_t stream)

@@ -754,9 +754,8 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
         }();
         if (!enough) return HIF4_ERR_UNSUPPORTED;
     }
-    // cheap enough to set on every call, and then right on every device
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CF::SMEM);
-    if (e != cudaSuccess) return cuda_failed(e);
+    const hif4_status st = allow_smem(reinterpret_cast<const void *>(k), CF::SMEM);
+    if (st != HIF4_OK) return st;
 
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(CF::THREADS);

@@ -139,15 +139,24 @@ __device__ __forceinline__ void load_params(const void *p, uint32_t bf16, int co
     for (int i = 0; i < 4; ++i) v[i] = pack2(e[2 * i], e[2 * i + 1]);
 }
 
-// Sum over the first nw lanes (the others hold 0), given to all.
-__device__ __forceinline__ float warps_sum(float v, int nw)
+// Sum over the first N lanes (the others hold 0), given to all.
+template <int N>
+__device__ __forceinline__ float warps_sum(float v)
 {
-    if (nw > 16) v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-    if (nw > 8) v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-    if (nw > 4) v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
-    if (nw > 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o < N) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
+// N maxima (NaN above all) over groups of W lanes, side by side.
+template <int W, int N>
+__device__ __forceinline__ void group_maxs(float (&v)[N])
+{
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = max_nan(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
 }
 
 // ---- the rows in flight: `depth` stages of [piece][thread] 16-byte pieces, each
@@ -220,14 +229,16 @@ template <bool XB, int OUT, int V, int LANES, int WIDE>
 __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 : 1) k_norm_fwd(NormArgs a)
 {
     constexpr int kDepth = depth<XB>(WIDE, V, 1), P = pieces<XB>(), ESZ = XB ? 2 : 4;
+    constexpr int OSZ = OUT == OUT_BF16 ? 2 : OUT == OUT_F32 ? 4 : 1;
+    constexpr int NW = WIDE ? WIDE / 32 : 1;
     extern __shared__ uint4 smem_rows[];
-    __shared__ float2 sStat[WIDE ? 2 : 1][32];
+    __shared__ float4 sStat[WIDE ? 2 : 1][NW];                  // (n, mean, M2, sum) of each warp's part
+    if (WIDE && threadIdx.x < 2 * NW) (&sStat[0][0])[threadIdx.x] = make_float4(0, 0, 0, 0);
     pdl_enter();
     const int T = WIDE ? blockDim.x : LANES;
     const int t = WIDE ? threadIdx.x : threadIdx.x % LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rpb = WIDE ? 1 : kSmallThreads / LANES;           // rows in flight per block
-    const int nw = blockDim.x >> 5;
     const int nt = blockDim.x;
     const bool tail = a.cols & 7;
 
@@ -242,7 +253,6 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
     uint4 *ring = smem_rows + threadIdx.x;                       // [kDepth][V][P][nt]
     const uint8_t *src = static_cast<const uint8_t *>(a.x) + ((int64_t)row * a.ldx + t * 8) * ESZ;
     const int64_t src_step = (int64_t)step * a.ldx * ESZ;
-    constexpr int OSZ = OUT == OUT_BF16 ? 2 : OUT == OUT_F32 ? 4 : 1;
     uint8_t *dst = static_cast<uint8_t *>(a.y) + ((int64_t)row * a.ldy + t * 8) * OSZ;
     const int64_t dst_step = (int64_t)step * a.ldy * OSZ;
     int frow = row;                                              // the next row to fetch
@@ -272,18 +282,15 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
         load_params(a.gamma, a.param_bf16, (t + v * T) * 8, valid[v], 1.0f, gm[v]);
         load_params(a.beta, a.param_bf16, (t + v * T) * 8, valid[v], 0.0f, bt[v]);
     }
-    // elements of a row in this warp's (or group's) part, and in that of warp `lane`
-    float n_w = 0.0f, n_l = 0.0f;
+    float n_w = 0.0f;                                            // elements of a row in this warp's (group's) part
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        n_w += (float)valid[v];
-        if (WIDE && lane < nw) n_l += (float)max(0, min(256, a.cols - (lane * 32 + v * T) * 8));
-    }
+    for (int v = 0; v < V; ++v) n_w += (float)valid[v];
     n_w = group_sum<LANES>(n_w);
-    const float inv_n_w = n_w > 0.0f ? 1.0f / n_w : 0.0f, inv_n_l = n_l > 0.0f ? 1.0f / n_l : 0.0f;
+    const float inv_n_w = n_w > 0.0f ? 1.0f / n_w : 0.0f;
 
     uint32_t bad = 0;
     int buf = 0, stage = 0;
+    if (WIDE) __syncthreads();                                   // sStat is cleared
     for (; wrow < a.rows;) {
         const bool live = row < a.rows;
         fetch((stage + kDepth - 1) % kDepth);
@@ -319,12 +326,13 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
         }
         m2 = group_sum<LANES>(m2);
         if (WIDE) {
-            if (lane == 0) sStat[buf][warp] = make_float2(sum_w, m2);
+            if (lane == 0) sStat[buf][warp] = make_float4(n_w, mean, m2, sum_w);
             __syncthreads();
-            const float2 p = lane < nw ? sStat[buf][lane] : make_float2(0.0f, 0.0f);
-            mean = warps_sum(p.x, nw) * a.inv_cols;
-            const float d = p.x * inv_n_l - mean;
-            m2 = warps_sum(fmaf(n_l * d, d, p.y), nw);
+            // lane w holds warp w's part; warps that do not exist count 0 elements
+            const float4 p = lane < NW ? sStat[buf][lane] : make_float4(0, 0, 0, 0);
+            mean = warps_sum<NW>(p.w) * a.inv_cols;
+            const float d = p.y - mean;
+            m2 = warps_sum<NW>(fmaf(p.x * d, d, p.z));
             buf ^= 1;
         }
         const float rstd = __frsqrt_rn(fmaf(m2, a.inv_cols, a.eps));
@@ -343,27 +351,26 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
                 y[v][2 * i + 1] = e.y;
             }
         if (OUT == OUT_BF16 || OUT == OUT_F32) {
+            if (live) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (live && valid[v] > 0)
-                    store8<OUT == OUT_BF16>(dst, v * T * 8, y[v], valid[v]);
+                for (int v = 0; v < V; ++v)
+                    if (valid[v] > 0) store8<OUT == OUT_BF16>(dst, v * T * 8, y[v], valid[v]);
+            }
         } else {
             constexpr int W = LANES < 16 ? LANES : 16;           // lanes of a 128-block
             float m[V];
             bool ok = true;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (!live || valid[v] < 8) {
+                const int n = live ? valid[v] : 0;
+                if (n < 8) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (!live || i >= valid[v]) y[v][i] = 0.0f;
+                        if (i >= n) y[v][i] = 0.0f;
                 }
                 m[v] = amax8_nan(y[v]);
             }
-#pragma unroll
-            for (int o = W / 2; o; o >>= 1)
-#pragma unroll
-                for (int v = 0; v < V; ++v) m[v] = max_nan(m[v], __shfl_xor_sync(0xFFFFFFFFu, m[v], o));
+            group_maxs<W, V>(m);
 #pragma unroll
             for (int v = 0; v < V; ++v) ok = ok && m[v] <= 3.402823466e38f;      // false for NaN too
             if (!__all_sync(0xFFFFFFFFu, ok)) {                  // rare: map what is not finite, and again
@@ -371,11 +378,10 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
                 for (int v = 0; v < V; ++v) {
                     sanitize_all(y[v], bad);
                     m[v] = amax8_nan(y[v]);
-#pragma unroll
-                    for (int o = W / 2; o; o >>= 1) m[v] = max_nan(m[v], __shfl_xor_sync(0xFFFFFFFFu, m[v], o));
                 }
+                group_maxs<W, V>(m);
             }
-            // lane 2 v forms the factor of the block of granule v, lane 2 v + 1 its scale
+            // lane 2 v of a block's lanes forms the factor of granule v's block, lane 2 v + 1 its scale
             const int l = t % W;
             float mine = m[0];
 #pragma unroll
@@ -383,15 +389,13 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
             const float s8 = scale_or_factor(f_bits(mine), fmt_max(OUT == OUT_E5M2 ? HIF4_E5M2 : HIF4_E4M3), l & 1);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int col = (t + v * T) * 8;
                 const float f = __shfl_sync(0xFFFFFFFFu, s8, 2 * v, W);
                 const uint32_t lo = encode4<OUT == OUT_E5M2>(y[v][0], y[v][1], y[v][2], y[v][3], f);
                 const uint32_t hi = encode4<OUT == OUT_E5M2>(y[v][4], y[v][5], y[v][6], y[v][7], f);
-                if (live && valid[v] > 0)
-                    store_codes8(dst + v * T * 8, lo, hi, valid[v]);
-                if (live && l == 2 * v + 1 && col - l * 8 < a.cols)
-                    a.scale[(int64_t)(col / BLK) * a.lds + row] = s8;
+                if (live && valid[v] > 0) store_codes8(dst + v * T * 8, lo, hi, valid[v]);
             }
+            const int c = (t - l + (l >> 1) * T) * 8;            // first column of the lane's block
+            if ((l & 1) && (l >> 1) < V && c < a.cols && live) a.scale[(int64_t)(c / BLK) * a.lds + row] = s8;
         }
         row += step;
         wrow += step;
@@ -401,11 +405,12 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
 }
 
 template <bool XB, int V, int LANES, int WIDE>
-__global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 ? 2 : 1) k_norm_bwd(NormBwdArgs a)
+__global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 && XB ? 2 : 1) k_norm_bwd(NormBwdArgs a)
 {
     constexpr int kDepth = depth<XB>(WIDE, V, 2), P = pieces<XB>(), ESZ = XB ? 2 : 4;
     extern __shared__ uint4 smem_rows[];
-    __shared__ float2 sSum[WIDE ? 2 : 1][32];
+    constexpr int NW = WIDE ? WIDE / 32 : 1;
+    __shared__ float2 sSum[WIDE ? 2 : 1][NW];
     pdl_enter();
     const int T = WIDE ? blockDim.x : LANES;
     const int t = WIDE ? threadIdx.x : threadIdx.x % LANES;
@@ -489,8 +494,8 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 ? 2 :
             if (lane == 0) sSum[buf][warp] = make_float2(t1, t2);
             __syncthreads();
             const float2 p = lane < nw ? sSum[buf][lane] : make_float2(0.0f, 0.0f);
-            t1 = warps_sum(p.x, nw);
-            t2 = warps_sum(p.y, nw);
+            t1 = warps_sum<NW>(p.x);
+            t2 = warps_sum<NW>(p.y);
             buf ^= 1;
         }
         if (a.dx) {
@@ -603,8 +608,8 @@ Shape shape_of(int64_t cols, int wide_v)
 template <typename A>
 hif4_status grid_of(void (*k)(A), const Shape &sh, int rows, size_t smem, int64_t &grid)
 {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_failed(e);
+    const hif4_status st = allow_smem(reinterpret_cast<const void *>(k), smem);
+    if (st != HIF4_OK) return st;
     const int rpb = sh.wide ? 1 : kSmallThreads / sh.lanes;
     grid = ((int64_t)rows + rpb - 1) / rpb;
     const int64_t most = (int64_t)sm_count() * blocks_per_sm(reinterpret_cast<const void *>(k), sh.threads, smem);
