@@ -20,10 +20,10 @@
 //     1 x 13824 x 5120 in 15.9 us, 4.5 TB/s, of which about 4 us are launch,
 //     first load and stores.
 //   128 x 128 tiles: short products of more rows.
-//   PAIR: 256 x 256 tiles of a cluster of two CTAs (tcgen05 cta_group::2).
-//     Each CTA loads 128 rows of P and 128 of Q, 32 KB a unit instead of the
-//     48 KB of a 128 x 256 tile: an SM takes in about 61 bytes a cycle, and a
-//     unit is 512 cycles of MMA.
+//   PAIR: 256 x 256 or 256 x 192 tiles of a cluster of two CTAs (tcgen05
+//     cta_group::2).  Each CTA loads 128 rows of P and half of Q's, 32 KB a unit
+//     for the larger tile instead of the 48 KB of a 128 x 256 tile: an SM takes
+//     in about 61 bytes a cycle, and a unit is 512 cycles of MMA.
 //
 // When there are too few tiles for the GPU, a cluster of S CTAs shares a tile:
 // each takes a contiguous part of K, leaves its FP32 totals in its shared
@@ -74,17 +74,18 @@ struct Cfg {
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int ACC = BN / EPI_WGS;    // totals per promotion thread
     static constexpr int CTAS = BN <= 32 ? 2 : 1;                // per SM
-    static constexpr int STAGES = PAIR ? 6 : 5;
+    static constexpr int STAGES = PAIR ? (BN > 192 ? 6 : 7) : 5;
     static constexpr int CH = 16;                // columns per TMEM read
     static constexpr int NCH = ACC / CH;
     // registers: the promotion warps take what the producer's warpgroup gives back; the shares add up to
     // what the launch brings along, 384 threads x 168
-    static constexpr int REG_LOW = BN >= 256 ? 72 : 0;
-    static constexpr int REG_HIGH = BN >= 256 ? 216 : 0;
+    static constexpr int REG_LOW = BN >= 192 ? 72 : 0;
+    static constexpr int REG_HIGH = BN >= 192 ? 216 : 0;
     static constexpr int P_BYTES = BP * KU;
     static constexpr int Q_BYTES = BN * KU / (PAIR ? 2 : 1);
     static constexpr int RING = STAGES * (P_BYTES + Q_BYTES);
-    static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int TMEM_COLS = BN > 128 ? 512 : 2 * BN;         // a power of two
+    static constexpr bool TWO_BLOCKS = BN == 192;                     // a thread's columns lie in up to two blocks of b
     static constexpr int BARS = 2 * STAGES + 4 + 2 + 2 * SLOTS;
     static constexpr bool PVEC = !SWAP || VECB, QVEC = SWAP || VECB;  // P / Q carry scale vectors
     static constexpr int PV = PVEC ? SLOTS * SG * BP : 0, QV = QVEC ? SLOTS * SG * BN : 0;
@@ -526,19 +527,26 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             float acc[C::ACC];
 #pragma unroll
             for (int j = 0; j < C::ACC; ++j) acc[j] = 0.0f;
-            // block scales: of the tile's 128 rows of b (SWAP: P; ACC <= 128 columns lie in one block)
-            const float *blk =
-                VECB ? nullptr : g.blk + min(SWAP ? pb : (qb * BN + c0) / 128, g.blk_rows - 1) * g.blk_ld;
+            // block scales: of the tile's 128 rows of b (SWAP), of this thread's columns, which lie in one
+            // block (ACC 64, 128) or have their second block begin `turn` columns on
+            const int first = SWAP ? pb : (qb * BN + c0) / 128;
+            const float *blk = VECB ? nullptr : g.blk + min(first, g.blk_rows - 1) * g.blk_ld;
+            const float *blk2 = VECB ? nullptr : g.blk + min(first + 1, g.blk_rows - 1) * g.blk_ld;
+            const int turn = 128 - (qb * BN + c0) % 128;
             // Lane l holds those of units u0 + 32 i + l: a global load for each unit would cost its whole
             // latency, since the wait for the accumulator's reads waits for it too.
-            float bs = 1.0f;
+            float bs = 1.0f, bs2 = 1.0f;
             for (int u = u0; u < u1; u += SG) {
-                if (!VECB && ((u - u0) & 31) == 0) bs = u + lane < u1 ? __ldg(blk + u + lane) : 0.0f;
+                if (!VECB && ((u - u0) & 31) == 0) {
+                    bs = u + lane < u1 ? __ldg(blk + u + lane) : 0.0f;
+                    if (C::TWO_BLOCKS) bs2 = u + lane < u1 ? __ldg(blk2 + u + lane) : 0.0f;
+                }
                 ok = mbar_wait_spin(&sfull[slot], sphase, abort_flag, g.timeout_ns);
-                float rc[SG];
+                float rc[SG], rc2[SG];
 #pragma unroll
                 for (int i = 0; i < SG; ++i) {
                     rc[i] = PVEC ? sPv[(slot * SG + i) * BP + prow] : 1.0f;
+                    if (C::TWO_BLOCKS && !VECB) rc2[i] = rc[i] * __shfl_sync(0xFFFFFFFFu, bs2, ((u - u0) & 31) + i);
                     if (!VECB) rc[i] *= __shfl_sync(0xFFFFFFFFu, bs, ((u - u0) & 31) + i);
                 }
                 const float *cv = sQv + slot * SG * BN + c0;
@@ -570,7 +578,8 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                                         mbar_arrive(&tempty[b]);
                                 }
                             }
-                            promote<C::CH, QVEC>(acc + c * C::CH, d, rc[i], cv + i * BN + c * C::CH);
+                            const float f = C::TWO_BLOCKS && !VECB && c * C::CH >= turn ? rc2[i] : rc[i];
+                            promote<C::CH, QVEC>(acc + c * C::CH, d, f, cv + i * BN + c * C::CH);
                         }
                     }
                 }
@@ -797,19 +806,23 @@ hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
 {
     if (c.M <= 16) return launch<16, true, VECB, false>(c, g, s);
     if (c.M <= 32) return launch<32, true, VECB, false>(c, g, s);
-    // 128 x 128 tiles of one CTA or 256 x 256 tiles of a pair, by estimated time in ns: a wave of tiles
-    // costs its units and its stores.  The pair's unit takes longer but is four times the work and needs
-    // half the operand bytes per product; the smaller tiles fill the SMs better and may share K.  Measured
-    // (us, small / pair): 128 x 5120 x 5120 12.8 / 23.8, 512 x 5120 x 13824 67.6 / 57.1, 1024 x 5120 x 5120
-    // 41.5 / 45.4, 1024 x 13824 x 5120 83.2 / 73.3, 8192 x 13824 x 5120 620 / 560.
-    const int64_t units = f8::blocks_of(c.K), sms = sm_count();
-    const int64_t small = f8::blocks_of(c.M) * f8::blocks_of(c.N);
-    const int64_t wide = ((c.M + 255) / 256) * ((c.N + 255) / 256);
+    // 128 x 128 tiles of one CTA, or 256 x 192 or 256 x 256 tiles of a pair, by estimated time in ns: each
+    // wave of tiles takes its units and its stores.  The larger a tile, the less a product costs in operand
+    // bytes and hand-offs; the smaller, the better the waves fill the SMs, and only the smallest share K.
+    // Measured (us; 128 x 128 / 256 x 192 / 256 x 256): 128 x 5120 x 5120 12.9 / 19.5 / 23.4,
+    // 512 x 5120 x 13824 68.3 / 50.6 / 57.8, 768 x 5120 x 13824 70.5 / 88.2 / 58.7, 1024 x 5120 x 5120
+    // 40.4 / 38.3 / 44.6, 2048 x 13824 x 5120 165 / 147 / 142, 8192 x 5120 x 13824 628 / 575 / 544.
+    // A unit takes longer where b has a scale per row: two operations per element instead of one.
+    const int64_t units = f8::blocks_of(c.K), sms = sm_count(), pairs = sms / 2;
+    const int64_t small = f8::blocks_of(c.M) * f8::blocks_of(c.N), rows2 = (c.M + 255) / 256;
+    const int64_t mid = rows2 * ((c.N + 191) / 192), wide = rows2 * ((c.N + 255) / 256);
     const int64_t share = small * 2 > sms ? 1 : sms / small < 8 ? sms / small : 8;
-    const int64_t t_small = ((small + sms - 1) / sms) * (units / share * 290 + 1500);
-    const int64_t t_wide = ((wide * 2 + sms - 1) / sms) * (units * 490 + 1800);
-    if (t_wide < t_small) return launch<256, false, VECB, true>(c, g, s);
-    return launch<128, false, VECB, false>(c, g, s);
+    const int64_t t_small = (small + sms - 1) / sms * (units / share * (VECB ? 455 : 290) + 1500);
+    const int64_t t_mid = (mid + pairs - 1) / pairs * (units * (VECB ? 640 : 415) + 1900);
+    const int64_t t_wide = (wide + pairs - 1) / pairs * (units * (VECB ? 830 : 475) + 2200);
+    if (t_small <= t_mid && t_small <= t_wide) return launch<128, false, VECB, false>(c, g, s);
+    if (t_mid < t_wide) return launch<192, false, VECB, true>(c, g, s);
+    return launch<256, false, VECB, true>(c, g, s);
 }
 
 } // namespace gemm8b

@@ -136,8 +136,10 @@ def operand(H, rng, rows, K, fmt, block):
 GEMMS = [(1, 128, 128), (1, 1, 1), (1, 300, 1000), (2, 256, 4096), (7, 100, 129), (16, 512, 640), (17, 130, 640),
          (32, 257, 2048), (33, 384, 100), (64, 1000, 512), (65, 128, 128), (100, 300, 777), (128, 256, 1152),
          (129, 129, 64), (200, 333, 1000), (256, 512, 512), (300, 264, 2048), (513, 640, 384),
-         # many short tiles: the CTA pairs; 2305 = 9 x 256 + 1 leaves a pair's second CTA without a row
-         (2305, 2817, 129), (2560, 2500, 300), (2400, 2600, 1024)]
+         # enough tiles for the CTA pairs, 192 and 256 columns wide; 256 k + 1 rows leave a pair's second
+         # CTA without one
+         (2305, 2817, 129), (2560, 2500, 300), (2400, 2600, 1024), (513, 3716, 100), (769, 3457, 100),
+         (770, 3100, 1100), (900, 3600, 1100)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMMS)
