@@ -9,6 +9,16 @@
 // column sums, stay in registers for the life of a block, and a block takes
 // rows b, b + grid, ...
 //
+// Measured (device time): forward 57600 x 5120 BF16, FP32 parameters, with
+// statistics: 195 us, 6.05 TB/s, 0.92 of the copy bandwidth.  Four granules a
+// thread (160 threads a row, three CTAs per SM): with two (320 threads) 232 us,
+// since a row's shuffles and reciprocal are paid once per warp; two rows side
+// by side on two granules each 262 us; next row prefetched in registers 263 us.
+// FP8 output 250 us, 0.55: bound by issue slots and the longer chain of a row
+// (about 630 instructions per warp and row), still less than the norm and the
+// quantizer one after the other (345 us).  Backward 335 us, 0.81 (two granules
+// a thread; with four its 200 registers leave one CTA per SM: 495 us).
+//
 // A thread fetches its own granules up to three rows ahead with cp.async into
 // its own places of shared memory: no barrier, no registers for data in flight,
 // and a granule that the row ends in is filled up with zeros by the copy.

@@ -11,6 +11,10 @@ higptq times HiGPTQ scheme one on an --n x --channels weight with the
 Hessian of --tokens activation rows (the Hessian itself untimed);
 fake_quantize_x is the FFN step's first call: --tokens x --channels
 activations with 1 % protected channels.
+quantize_f8 | quantize_f8_both | gemm_f8_block | gemm_f8_block_wgrad | norm | norm_f8 |
+norm_bwd are the block-scaled FP8 calls and the layer norm on --tokens x
+--channels activations (both layouts of an output gradient; the product with
+an --n x --channels weight; the weight gradient, whose depth is --tokens).
 Sizes default to small cases that still exceed the 126 MB L2 (a few hundred
 MB on the device).  Prints the mean CUDA-event time per call.
 """
@@ -23,7 +27,8 @@ import sys
 def main(argv=None):
     p = argparse.ArgumentParser()
     p.add_argument("op", choices=["quantize", "dequantize", "fake_quantize", "fake_quantize_x", "gemm", "gemm_gelu",
-                                  "gemm_fq", "calib", "linear", "ffn", "higptq"])
+                                  "gemm_fq", "calib", "linear", "ffn", "higptq", "quantize_f8", "quantize_f8_both",
+                                  "gemm_f8_block", "gemm_f8_block_wgrad", "norm", "norm_f8", "norm_bwd"])
     p.add_argument("--log2n", type=int, default=28, help="elements for quantize/dequantize/fake_quantize")
     p.add_argument("--protect", type=float, default=0.01,
                    help="fake_quantize_x: fraction of protected channels (0 = no mask)")
@@ -67,6 +72,39 @@ def main(argv=None):
                          device=dev)
         fn = lambda: H.higptq1(w, Hm, None, 0.01, a.blocksize, workspace=ws)  # noqa: E731
         nbytes = 2.0 * a.n * a.channels * a.channels / 2        # FLOPs of the lazy updates (N K^2 / 2 FMA)
+    elif a.op.startswith(("quantize_f8", "gemm_f8_block", "norm")):
+        x, _ = wl.device_rows(a.tokens, a.channels, seed=3, device=dev)
+        gamma, beta = torch.ones(a.channels, device=dev), torch.zeros(a.channels, device=dev)
+        n = float(a.tokens) * a.channels
+        if a.op == "quantize_f8":
+            out = H.quantize_f8(x)
+            fn, nbytes = (lambda: H.quantize_f8(x, out=out)), 3 * n
+        elif a.op == "quantize_f8_both":
+            out = H.quantize_f8(x, torch.float8_e5m2, layout="both")
+            fn, nbytes = (lambda: H.quantize_f8(x, torch.float8_e5m2, layout="both", out=out)), 4 * n
+        elif a.op == "norm":
+            out = torch.empty_like(x)
+            fn, nbytes = (lambda: H.layer_norm(x, gamma, beta, out=out)), 4 * n
+        elif a.op == "norm_f8":
+            out = H.layer_norm_f8(x, gamma, beta)
+            fn, nbytes = (lambda: H.layer_norm_f8(x, gamma, beta, out=out)), 3 * n
+        elif a.op == "norm_bwd":
+            dy, _ = wl.device_rows(a.tokens, a.channels, seed=7, device=dev)
+            _, mean, rstd = H.layer_norm(x, gamma, beta, save_stats=True)
+            out = H.layer_norm_backward(dy, x, mean, rstd, gamma)
+            fn, nbytes = (lambda: H.layer_norm_backward(dy, x, mean, rstd, gamma, out=out)), 6 * n
+        else:
+            if a.op == "gemm_f8_block":
+                q, w = H.quantize_f8(x), H.quantize_f8(wl.device_weight(a.n, a.channels, 0.015, seed=31, device=dev),
+                                                       block_rows=128)
+                out = torch.empty(a.tokens, a.n, dtype=torch.bfloat16, device=dev)
+            else:
+                dy, _ = wl.device_rows(a.tokens, a.n, seed=7, device=dev)
+                q, w = H.quantize_f8(dy, torch.float8_e5m2, layout="cols"), H.quantize_f8(x, layout="cols")
+                out = torch.empty(a.n, a.channels, device=dev)
+            rows = 128 if a.op == "gemm_f8_block" else 1
+            fn = lambda: H.gemm_f8_block(*q, *w, b_block_rows=rows, out=out)  # noqa: E731
+            nbytes = 2.0 * a.tokens * a.n * a.channels                         # FLOPs
     elif a.op == "calib":
         x = wl.calib_torch(a.tokens, a.channels, dev)
         ws = torch.empty(H.calib_workspace(a.tokens, a.channels), dtype=torch.uint8, device=dev)
@@ -106,7 +144,8 @@ def main(argv=None):
     e1.record()
     torch.cuda.synchronize()
     ms = e0.elapsed_time(e1) / a.reps
-    unit = "TFLOP/s" if a.op in ("gemm", "gemm_gelu", "gemm_fq", "linear", "ffn", "higptq") else "GB/s"
+    unit = "TFLOP/s" if a.op in ("gemm", "gemm_gelu", "gemm_fq", "linear", "ffn", "higptq",
+                               "gemm_f8_block", "gemm_f8_block_wgrad") else "GB/s"
     rate = nbytes / (ms * 1e-3) / (1e12 if unit == "TFLOP/s" else 1e9)
     print("%s: %.4f ms per call, %.1f %s" % (a.op, ms, rate, unit))
     return 0

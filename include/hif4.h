@@ -295,8 +295,9 @@ hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t rows, int6
  * and the next multiple of 4 never reaches y).
  * bias  NULL or BF16 [N].   y  BF16 (FP32 with HIF4_LINEAR_OUT_F32, the only
  *       flag) M x N, ldy.
- * For one to a few rows of a the weight is streamed once, K split over a
- * cluster of CTAs; the order of every sum is fixed.  Any M, N and K >= 1.
+ * For up to 32 rows of a the weight is streamed once, K split over a cluster
+ * of CTAs; the order of every sum is fixed.  Any M, N and K >= 1.  y may not
+ * overlap an input.
  * A NaN code makes the outputs that it reaches NaN.
  * Errors: SHAPE (K == 0 with M, N > 0; leading dimensions), ALIGNMENT,
  *         INVALID_ARG, UNSUPPORTED (sizes, or a layout the driver's
@@ -317,8 +318,9 @@ hif4_status hif4_gemm_f8_block(const uint8_t *a, hif4_f8_format a_fmt, int64_t M
  * gamma, beta  NULL (1, 0) or [cols] of param_dtype, naturally aligned.
  * mean, rstd   NULL or FP32 [rows] out: what the backward pass reads.
  * eps >= 0 and finite.  NaN and infinities propagate as in the formulas.
+ * y may be x itself where type and leading dimension are the same.
  * Errors: INVALID_ARG, SHAPE (ldx or ldy < cols), ALIGNMENT, UNSUPPORTED
- *         (cols > 16384).
+ *         (cols > 16384, rows > 2^30).
  */
 hif4_status hif4_layer_norm(const void *x, hif4_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
                             const void *gamma, const void *beta, hif4_dtype param_dtype, float eps, void *y,
@@ -343,6 +345,7 @@ hif4_status hif4_layer_norm_f8(const void *x, hif4_dtype dtype, int64_t rows, in
  *            the forward call left them; gamma as there.
  * dx, dgamma, dbeta  outputs, each may be NULL (not all); dgamma and dbeta
  *            FP32 [cols], written (not added to), zero for rows == 0.
+ * dx may be dy or x itself, with its leading dimension.
  * workspace  >= hif4_layer_norm_backward_workspace(rows, cols) bytes, 256-byte
  *            aligned, when dgamma or dbeta is wanted (the blocks' partial
  *            sums, joined in a fixed order); calls that overlap on the GPU
@@ -567,7 +570,7 @@ hif4_status hif4_ptq_state_unpack(const void *buf, size_t bytes, uint8_t *codes,
 /*
  * hif4_debug_wait_test — failure-handling diagnostic; off by default and not
  * meant for production runs.  Every wait of the TMA-fed kernels on an
- * asynchronous copy is bounded by wall time (4 s in the tcgen05 GEMM, 2 s in
+ * asynchronous copy is bounded by wall time (4 s in the tcgen05 GEMMs, 2 s in
  * the quantizers and the calibration passes): a block whose wait runs out
  * stops, lets the copies it issued land (and, in the GEMM, its MMAs
  * complete before the tensor memory is freed), and reports

@@ -104,25 +104,31 @@ def test_quantizer_is_exact(H, rows, cols, block, dt):
                 assert np.array_equal(host(q), want_q), (fmt, layout, direct)
 
 
-def test_quantizer_maps_nonfinite_and_reports_it(H):
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantizer_maps_nonfinite_and_reports_it(H, dt, block):
     import torch
     from block_floating_point_hif4_b200 import binding as B
-    x = np.random.default_rng(3).standard_normal((130, 200))
-    xd = on_gpu(x, torch.bfloat16)
+    xd = on_gpu(np.random.default_rng(3).standard_normal((130, 200)), dtype_of(dt))
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    for layout in ("rows", "both"):
-        H.quantize_f8(xd, layout=layout, status=st)
+    for layout in ("rows", "cols", "both"):
+        H.quantize_f8(xd, block_rows=block, layout=layout, status=st)
         assert H.get_status(st) == B.OK
     xd[5, 7] = float("nan")
     xd[129, 199] = float("inf")
     xd[6, 0] = float("-inf")
-    for layout in ("rows", "both"):
+    xd[7, 130] = float("nan")
+    x = host(xd)
+    for layout in ("rows", "cols", "both"):
         st.zero_()
-        q, s = H.quantize_f8(xd, layout=layout, status=st)[:2]
+        got = list(H.quantize_f8(xd, block_rows=block, layout=layout, status=st))
         assert H.get_status(st) == B.ERR_NONFINITE
-        want_q, want_s = R.quantize(host(xd), "e4m3", 1, 128)
-        assert np.array_equal(host(q), want_q) and np.array_equal(s.cpu().numpy(), want_s.T)
-        assert host(q)[5, 7] == 0 and host(q)[129, 199] == 448 and host(q)[6, 0] == -448
+        for direct in {"rows": (1,), "cols": (0,), "both": (1, 0)}[layout]:
+            q, s = host(got.pop(0)), got.pop(0).cpu().numpy()
+            want_q, want_s = R.quantize(x if direct else x.T, "e4m3", block, 128)
+            assert np.array_equal(q, want_q) and np.array_equal(s, want_s.T if block == 1 else want_s)
+            q = q if direct else q.T
+            assert q[5, 7] == 0 and q[7, 130] == 0 and q[129, 199] == 448 and q[6, 0] == -448
 
 
 def operand(H, rng, rows, K, fmt, block):

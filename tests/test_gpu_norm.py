@@ -157,6 +157,25 @@ def test_nonfinite_rows_stay_their_own(H):  # noqa: F811
         assert torch.all(q[7].float() == 0) and torch.all(q[9].float() == 0)
 
 
+def test_in_place(H):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(9)
+    for rows, cols in ((700, 96), (700, 640), (900, 2000), (400, 6000)):
+        for dt in ("bf16", "f32"):
+            x = on_gpu(rows_of(rng, rows, cols), dtype_of(dt))
+            dy = on_gpu(rng.standard_normal((rows, cols)), dtype_of(dt))
+            g, b = params(rng, cols, "f32")
+            y, mean, rstd = H.layer_norm(x, g, b, EPS, save_stats=True)
+            dx, dg, db = H.layer_norm_backward(dy, x, mean, rstd, g)
+            for t in (x, dy):
+                c = [u.clone(memory_format=torch.preserve_format) for u in (x, dy)]
+                c = [torch.empty(rows, x.stride(0), dtype=x.dtype, device="cuda")[:, :cols].copy_(u) for u in c]
+                o = H.layer_norm_backward(c[1], c[0], mean, rstd, g, out=(c[0] if t is x else c[1], dg, db))
+                assert torch.equal(o[0], dx)
+            assert H.layer_norm(x, g, b, EPS, out=x) is x
+            assert torch.equal(x, y)
+
+
 def test_no_rows(H):  # noqa: F811
     import torch
     x = torch.empty(0, 320, device="cuda")
@@ -268,6 +287,33 @@ def test_layer_captured_and_replayed_on_new_inputs(H):  # noqa: F811
     eager, _ = layer(H, x, dy, g, b, w)
     for got, want in zip(outs, eager):
         assert torch.equal(got, want)
+
+
+def test_pairs_captured_and_replayed(H):  # noqa: F811
+    """The products that run on CTA pairs, several in one graph, each replay on new operands."""
+    import torch
+    rng = np.random.default_rng(10)
+    x = on_gpu(rng.standard_normal((900, 1100)), dtype_of("bf16"))
+    w = on_gpu(rng.standard_normal((3600, 1100)), dtype_of("bf16"))
+    wq, ws = H.quantize_f8(w, block_rows=128)
+
+    def chain():
+        q, s = H.quantize_f8(x)
+        y = H.gemm_f8_block(q, s, wq, ws)
+        return y, H.gemm_f8_block(*H.quantize_f8(y[:700, :1100]), wq, ws, out_f32=True)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        chain()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = chain()
+    for _ in range(3):
+        x.neg_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(outs, chain()):
+            assert torch.equal(got, want)
 
 
 def test_layer_on_two_streams_at_once(H):  # noqa: F811
