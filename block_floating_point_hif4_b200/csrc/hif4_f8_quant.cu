@@ -23,6 +23,7 @@
 // 13824 x 5120 weight in 128 x 128 blocks, both layouts, 50.1 us, 0.86.  The
 // tiles are bound by issue slots (69 % busy) with 4 CTAs per SM.
 #include "hif4_f8.cuh"
+#include "hif4_pdl.cuh"
 
 namespace hif4 {
 namespace {
@@ -57,6 +58,7 @@ constexpr int kRowsPerCta = kThreads / 8;      // k_f8_rows: rows of a 128-colum
 template <bool BF16, bool E5M2>
 __global__ void __launch_bounds__(kThreads, BF16 ? 8 : 6) k_f8_rows(F8QuantArgs a)
 {
+    pdl_enter();
     const int l8 = threadIdx.x & 7, group = threadIdx.x >> 3;
     bool bad = false;
     for (uint32_t it = blockIdx.x; it < a.items; it += gridDim.x) {
@@ -189,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 2) k_f8_tile(F8QuantArgs 
     __shared__ __align__(16) uint8_t sT[BLK * BLK];
     __shared__ __align__(16) uint32_t sMax[kThreads / 32][BLK];
     __shared__ __align__(16) float sF[BLK];
+    pdl_enter();
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5;
     const uint32_t rb = a.nblk_div.div(blockIdx.x);
     const uint32_t cb = blockIdx.x - rb * a.nblk;
@@ -360,15 +363,12 @@ hif4_status launch_quant(F8QuantArgs &a, bool square, cudaStream_t s)
         a.items = (uint32_t)items;
         const void *k = reinterpret_cast<const void *>(k_f8_rows<BF16, E5M2>);
         const int64_t most = 8 * (int64_t)sm_count() * blocks_per_sm(k, kThreads, 0);
-        k_f8_rows<BF16, E5M2><<<(unsigned)(items < most ? items : most), kThreads, 0, s>>>(a);
-        return launch_status();
+        return launch_pdl(k_f8_rows<BF16, E5M2>, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), 0, s,
+                          a);
     }
-    const unsigned grid = (unsigned)(f8::blocks_of(a.rows) * cblk);
-    if (square)
-        k_f8_tile<BF16, true, E5M2><<<grid, kThreads, 0, s>>>(a);
-    else
-        k_f8_tile<BF16, false, E5M2><<<grid, kThreads, 0, s>>>(a);
-    return launch_status();
+    const dim3 grid((unsigned)(f8::blocks_of(a.rows) * cblk));
+    return square ? launch_pdl(k_f8_tile<BF16, true, E5M2>, grid, dim3(kThreads), 0, s, a)
+                  : launch_pdl(k_f8_tile<BF16, false, E5M2>, grid, dim3(kThreads), 0, s, a);
 }
 
 } // namespace
