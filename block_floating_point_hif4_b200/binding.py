@@ -463,13 +463,18 @@ def ptq_state_unpack(record: bytes, device=None):
 # ------------------------------------------------- block-scaled FP8, layer norm
 #
 # These calls are short enough for their marshalling to count: pointers are
-# passed as integers, a padded allocation is only sliced where it has padding,
-# and no context is entered where device and stream are the current ones.
+# passed as integers, padded tensors are allocated as such, and no context is
+# entered where device and stream are the current ones.
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 _F8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
 _SCALE = {torch.float32: F32}
 _BIAS = {torch.bfloat16: BF16}
+
+# the public calls build a Stream object, or check for a lazy start, each time
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _cdiv(n, m):
@@ -523,9 +528,8 @@ def _status(t):
 
 def _padded(rows, cols, dtype, multiple, device):
     """rows x cols whose leading dimension is a multiple of `multiple` elements."""
-    pad = -cols % multiple
-    t = torch.empty(rows, cols + pad, dtype=dtype, device=device)
-    return t[:, :cols] if pad else t
+    return torch.empty_strided((rows, cols), ((cols + multiple - 1) // multiple * multiple, 1), dtype=dtype,
+                               device=device)
 
 
 @contextlib.contextmanager
@@ -538,16 +542,16 @@ def _place(stream, *tensors):
     """Context of a call: its tensors' device current, `stream` (default: that
     device's current stream) current, so that what the call allocates belongs
     to the stream it runs on.  Yields the stream's handle."""
-    dev = tensors[0].device
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors of one call must be on one device")
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return contextlib.nullcontext(torch.cuda.current_stream(dev).cuda_stream)
-        stream = torch.cuda.current_stream(dev)
-    _need(stream.device == dev, "the stream is on another device than the tensors")
-    return _switched(dev, stream)
+        if index == _raw_device():
+            return contextlib.nullcontext(_raw_stream(index))
+        stream = torch.cuda.current_stream(index)
+    _need(stream.device.index == index, "the stream is on another device than the tensors")
+    return _switched(tensors[0].device, stream)
 
 
 def quantize_f8(x: torch.Tensor, fmt=torch.float8_e4m3fn, *, block_rows: int = 1, layout: str = "rows", out=None,
@@ -633,7 +637,8 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
         ldy = _matrix(out, "out", _DTYPE, (rows, cols))[2]
         mean = rstd = None
         if save_stats:
-            mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=x.device).unbind(0)
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         _check("hif4_layer_norm", lib().hif4_layer_norm(
             x.data_ptr(), _DTYPE[x.dtype], rows, cols, ldx, pg, pb, pdt, eps, out.data_ptr(), _DTYPE[out.dtype], ldy,
             mean.data_ptr() if save_stats else None, rstd.data_ptr() if save_stats else None, s))
@@ -657,7 +662,8 @@ def layer_norm_f8(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torc
         lds = _matrix(sc, "out[1]", _SCALE, (units, rows))[2]
         mean = rstd = None
         if save_stats:
-            mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=x.device).unbind(0)
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         _check("hif4_layer_norm_f8", lib().hif4_layer_norm_f8(
             x.data_ptr(), _DTYPE[x.dtype], rows, cols, ldx, pg, pb, pdt, eps, _F8[fmt], q.data_ptr(), ldq,
             sc.data_ptr(), lds, mean.data_ptr() if save_stats else None, rstd.data_ptr() if save_stats else None,
@@ -681,8 +687,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     pg, _, pdt = _norm_params(gamma, None, cols)
     with _place(stream, x, dy, mean, rstd, gamma, workspace, *(out if out is not None else ())) as s:
         if out is None:
-            out = (_padded(rows, cols, x.dtype, 8, x.device),
-                   *torch.empty(2, cols, dtype=torch.float32, device=x.device).unbind(0))
+            dev = x.device
+            out = (_padded(rows, cols, x.dtype, 8, dev), torch.empty(cols, dtype=torch.float32, device=dev),
+                   torch.empty(cols, dtype=torch.float32, device=dev))
         dx, dgamma, dbeta = out
         lddx = 0 if dx is None else _matrix(dx, "out[0]", {x.dtype: 0}, (rows, cols))[2]
         pdg, pdb = _vector(dgamma, "out[1]", _SCALE, cols), _vector(dbeta, "out[2]", _SCALE, cols)
