@@ -149,7 +149,7 @@ int blocks_per_sm(const void *kernel, int threads, size_t dyn_smem)
 
 hif4_status allow_smem(const void *kernel, size_t bytes)
 {
-    if (bytes <= 48 * 1024) return HIF4_OK;
+    if (bytes <= 32 * 1024) return HIF4_OK;         // 48 KB are allowed anyway, the kernel's static part included
     struct Entry {
         const void *kernel;
         int dev;

@@ -96,6 +96,28 @@ def test_backward(H, rows, cols, dt):  # noqa: F811
         assert torch.equal(db1, db)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_every_row_width_class(H, dt):  # noqa: F811
+    """Each number of warps that a row is spread over, forward, FP8 forward and backward."""
+    import torch
+    rng = np.random.default_rng(14)
+    for cols in list(range(72, 1025, 136)) + list(range(1032, 16385, 512)) + list(range(1536, 16385, 512)) + [5954]:
+        x = on_gpu(rng.standard_normal((3, cols)), dtype_of(dt))
+        dy = on_gpu(rng.standard_normal((3, cols)), dtype_of(dt))
+        g, b = params(rng, cols, "f32")
+        y, mean, rstd = H.layer_norm(x, g, b, EPS, out_dtype=torch.float32, save_stats=True)
+        want, wm, wr, e_y, e_m, e_r = R.norm(host(x), num(g), num(b), EPS)
+        R.assert_within(host(y), want, R.stored(e_y, want, "f32"), "y %d" % cols)
+        q, s = H.layer_norm_f8(x, g, b, EPS)
+        q2, s2 = H.quantize_f8(on_gpu(host(y), torch.float32))
+        assert torch.equal(s, s2) and np.array_equal(host(q), host(q2)), cols
+        dx, dg, db = H.layer_norm_backward(dy, x, mean, rstd, g)
+        want, wg, wb, e_dx, e_dg, e_db = R.norm_backward(host(dy), host(x), host(mean), host(rstd), num(g))
+        R.assert_within(host(dx), want, R.stored(e_dx, want, dt), "dx %d" % cols)
+        R.assert_within(host(dg), wg, e_dg, "dgamma %d" % cols)
+        R.assert_within(host(db), wb, e_db, "dbeta %d" % cols)
+
+
 @pytest.mark.parametrize("cols", [24, 200, 1300])
 def test_gradients_against_differences(H, cols):  # noqa: F811
     """Directional derivatives of L = sum(c y) by central differences of the 64-bit form."""
