@@ -613,12 +613,6 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
 #pragma unroll
                 for (int j = 0; j < C::ACC; ++j)
                     if (p < g.P && q0 + j < g.Q) store_one(g, q0 + j, p, acc[j] + bv);
-            } else {
-                if (g.bias) {
-#pragma unroll
-                    for (int j = 0; j < C::ACC; ++j)
-                        if (q0 + j < g.Q) acc[j] += bias_of(g, q0 + j);
-                }
             }
             if (!SWAP && !(C::SPLITS && split > 1)) {
                 // Rows leave through shared memory, 64 bytes of each of the warp's 32 rows at a time, so
@@ -626,6 +620,24 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 // of row r sits at piece i ^ (r / 2 % 4): no bank conflicts either way.
                 uint8_t *st = sSt + (warp - 4) * ST_BYTES;
                 const int64_t r0 = (int64_t)pb * BP + q4 * 32;
+                if (g.bias) {
+                    // The columns' biases pass through the same place: one load per lane and 32 columns,
+                    // not one per column (3641 x 8576 x 491, FP32 output: 98 -> 55 us).
+                    float *sb = reinterpret_cast<float *>(st);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < C::ACC; j += 32)
+                        sb[j + lane] = q0 + j + lane < g.Q ? bias_of(g, q0 + j + lane) : 0.0f;
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < C::ACC; j += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sb + j);
+                        acc[j] += v.x;
+                        acc[j + 1] += v.y;
+                        acc[j + 2] += v.z;
+                        acc[j + 3] += v.w;
+                    }
+                }
                 if (g.out_f32)
                     store_rows<C::ACC, 16, true>(g, st, acc, lane, r0, q0);
                 else
