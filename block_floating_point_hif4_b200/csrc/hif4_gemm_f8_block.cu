@@ -39,9 +39,9 @@
 // the FP32 scales cost.  A 128 x 256 tile of one CTA measured 3 to 8 % slower.
 //
 // Every mbarrier wait is bounded (4 s); a role that gives up sets the block's
-// abort flag, the producers let their copies land, the MMA warps drain their
-// MMAs before TMEM is freed, every thread still meets the cluster barriers,
-// and HIF4_FLAG_TIMEOUT is raised.
+// abort flag, the producers let their copies land and the arrivals of a pair's
+// other CTA come in, the MMA warps drain their MMAs before TMEM is freed, every
+// thread still meets the cluster barriers, and HIF4_FLAG_TIMEOUT is raised.
 #include <mutex>
 
 #include "hif4_f8.cuh"
@@ -62,7 +62,7 @@ constexpr int SLOTS = 2;
 constexpr int ST_BYTES = 2048;                 // a promotion warp's staging of its stores: 32 rows of 64 bytes
 constexpr int GROUP = 16;                       // raster: P tiles per group
 constexpr uint64_t TIMEOUT_NS = 4000000000ull;
-constexpr uint64_t DRAIN_NS = 100000000ull;
+constexpr uint64_t DRAIN_NS = 20000000ull;
 
 // BN: columns of the tile.  PAIR: two CTAs share a tile of 256 rows (each holds 128 of them and half of
 // Q's rows).
@@ -395,23 +395,15 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     }
                 }
             }
-            if (PAIR && ok) {
-                // the issuing CTA's arrivals on this CTA's barriers come in before it leaves
-                for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
-                    const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
-                    const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-                    mbar_wait_bounded(&empty[s], ph, abort_flag, g.timeout_ns);
-                }
-            }
-            if (!ok) {
-                // let our own copies land before the block leaves; a pair's second CTA cannot see the
-                // barrier that its copies complete on, and waits the same time
-                for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
-                    const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
-                    const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-                    mbar_wait_bounded(&full[s], ph, nullptr, DRAIN_NS);
-                    if (PAIR && rank > 0) break;
-                }
+            // Whether the tiles are done or a wait gave up: the copies land before the block leaves, and so do
+            // the issuing CTA's arrivals on a second CTA's barriers (whose copies complete on the issuing
+            // CTA's).  Neither wait looks at the abort flag: after a time-out the MMA warps may still issue a
+            // unit that the promotion warps' last hand-off lets through, and its arrivals come late.
+            for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
+                const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
+                const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
+                if (!PAIR || rank == 0) mbar_wait_bounded(&full[s], ph, nullptr, DRAIN_NS);
+                if (PAIR) mbar_wait_bounded(&empty[s], ph, nullptr, DRAIN_NS);
             }
         } else if (warp == 3) {
             // ---------------------------------------------------- scales
@@ -448,9 +440,9 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     }
                 }
             }
-            if (!ok)                            // let the copies in flight land
-                for (uint32_t s = 0; s < (uint32_t)SLOTS; ++s)
-                    mbar_wait_bounded(&sfull[s], s < slot ? phase : (phase ^ 1u), nullptr, DRAIN_NS);
+            // (a slot that was never filled counts as landed: its barrier's phase before the first)
+            for (uint32_t s = 0; s < (uint32_t)SLOTS; ++s)
+                mbar_wait_bounded(&sfull[s], s < slot ? phase : (phase ^ 1u), nullptr, DRAIN_NS);
         } else if (!PAIR || rank == 0) {
             // ---------------------------------------------------- MMA issuers
             // One warp for each accumulator: issuing a unit's MMAs and commits takes one thread as long
