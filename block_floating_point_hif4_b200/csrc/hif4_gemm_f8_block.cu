@@ -7,8 +7,12 @@
 // two), so each 128-deep product ("unit") goes to a TMEM accumulator of its own
 // (tcgen05 kind::f8f6f4, FP32 accumulation), and promotion warps read it back
 // and add  scale * P  into FP32 totals held in registers: one FMA per output
-// element and unit (two where b has a scale per row, whose product with a's is
-// formed in the same place).
+// element and unit, and a multiplication where b has a scale per row, for its
+// product with a's.  There a thread holds four rows of a quarter of the columns
+// (16x256b reads) and not one row (32x32b): a scale read from shared memory
+// serves four rows, else those reads take longer than the MMAs (5120 x 5120 x
+// 14391: 592 us with one row per thread, 489 with four; without the scales'
+// reads and products, in a trial copy, 440).
 //
 // Roles: warp 0 issues the TMA loads (128-byte swizzled operand tiles into a
 // ring), warps 1 and 2 the MMAs into two alternating accumulators, warp 3 the
@@ -75,8 +79,9 @@ struct Cfg {
     static constexpr int ACC = BN / EPI_WGS;    // totals per promotion thread
     static constexpr int CTAS = BN <= 32 ? 2 : 1;                // per SM
     static constexpr int STAGES = PAIR ? (BN > 192 ? 6 : 7) : 5;
-    static constexpr int CH = 16;                // columns per TMEM read
+    static constexpr int CH = 16;                // values per thread and TMEM read
     static constexpr int NCH = ACC / CH;
+    static constexpr bool FRAG = VECB && !SWAP; // a thread's totals are those of 4 rows, not of one
     // registers: the promotion warps take what the producer's warpgroup gives back; the shares add up to
     // what the launch brings along, 384 threads x 168
     static constexpr int REG_LOW = BN >= 192 ? 72 : 0;
@@ -124,13 +129,13 @@ __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, f
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N])
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1)
 {
-    if constexpr (N == 32)
-        sm100::tmem_ld_32x32b_x32(addr, r);
-    else
-        sm100::tmem_ld_32x32b_x16(addr, r);
+    asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 // Waits for the TMEM reads in flight; r may be used only after it.
@@ -190,7 +195,7 @@ __device__ __forceinline__ void tile_coords(int t, const Args &g, int &pb, int &
 }
 
 // Stores the N totals of each of a warp's 32 rows (r0 + lane), W columns (64 bytes) at a time.
-template <int N, int W, bool F32>
+template <int N, int W, bool F32, bool FRAG>
 __device__ __forceinline__ void store_rows(const Args &g, uint8_t *st, const float (&acc)[N], int lane, int64_t r0,
                                            int q0)
 {
@@ -200,8 +205,21 @@ __device__ __forceinline__ void store_rows(const Args &g, uint8_t *st, const flo
     for (int j = 0; j < N; j += W) {
         if (q0 + j >= g.Q) break;
         __syncwarp();
+        if constexpr (FRAG) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < W / 2; ++i) {   // 8 columns n of row r, two of them in this thread
+                const int n = i % (W / 8), r = i / (W / 8) * 8 + row;
+                const float *v = acc + (j / 32 * 2 + i / (W / 4)) * 16 + (j % 32 / 8 + n) * 4 + (i / (W / 8) & 1) * 2;
+                const int at = F32 ? n * 2 + piece / 2 : n;     // the 16-byte piece they belong to
+                uint8_t *d = st + r * 64 + ((at ^ (r >> 1)) & 3) * 16;
+                if (F32)
+                    *reinterpret_cast<float2 *>(d + (piece & 1) * 8) = make_float2(v[0], v[1]);
+                else
+                    *reinterpret_cast<uint32_t *>(d + piece * 4) = f8::pack_bf16_rn(v[0], v[1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 && !FRAG; ++i) {
             uint4 w;
             const float *v = acc + j + i * (W / 4);
             if (F32)
@@ -252,6 +270,17 @@ __device__ __forceinline__ void promote(float *acc, const uint32_t (&p)[N], floa
 #pragma unroll
         for (int i = 0; i < 4; i += 2)
             fma2(acc[j + i], acc[j + i + 1], bits_f(p[j + i]), bits_f(p[j + i + 1]), f[i], f[i + 1]);
+    }
+}
+
+// The factors of the 16 values that a read of 16 rows and 32 columns leaves in a thread: rows l / 4 (scale r[0])
+// and l / 4 + 8 (r[1]) of four pairs of columns (scales w).
+__device__ __forceinline__ void frag_factors(float (&f)[16], const float *r, const float2 (&w)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        mul2(f[4 * k], f[4 * k + 1], w[k].x, w[k].y, r[0], r[0]);
+        mul2(f[4 * k + 2], f[4 * k + 3], w[k].x, w[k].y, r[1], r[1]);
     }
 }
 
@@ -536,7 +565,7 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 ok = mbar_wait_spin(&sfull[slot], sphase, abort_flag, g.timeout_ns);
                 float rc[SG], rc2[SG];
 #pragma unroll
-                for (int i = 0; i < SG; ++i) {
+                for (int i = 0; i < SG && !C::FRAG; ++i) {
                     rc[i] = PVEC ? sPv[(slot * SG + i) * BP + prow] : 1.0f;
                     if (C::TWO_BLOCKS && !VECB) rc2[i] = rc[i] * __shfl_sync(0xFFFFFFFFu, bs2, ((u - u0) & 31) + i);
                     if (!VECB) rc[i] *= __shfl_sync(0xFFFFFFFFu, bs, ((u - u0) & 31) + i);
@@ -553,25 +582,62 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                         ok &= mbar_wait_spin(&tfull[b], tph, abort_flag, g.timeout_ns);
                         tph ^= 1u;
                         tc_fence_after();
-                        // One chunk in flight for each warp: the two warps of a scheduler take turns at
-                        // reading and adding.
-#pragma unroll
-                        for (int c = 0; c < C::NCH; ++c) {
-                            uint32_t d[C::CH];
-                            tmem_load<C::CH>(ta + b * BN + c * C::CH, d);
-                            tmem_landed<C::CH>(d);
-                            if (c + 1 == C::NCH) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) {
-                                    if (PAIR)
-                                        mbar_arrive_remote(rel + b * 8);
-                                    else
-                                        mbar_arrive(&tempty[b]);
-                                }
+                        // the accumulator is free once its last read has landed
+                        const auto release = [&] {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (PAIR)
+                                    mbar_arrive_remote(rel + b * 8);
+                                else
+                                    mbar_arrive(&tempty[b]);
                             }
-                            const float f = C::TWO_BLOCKS && !VECB && c * C::CH >= turn ? rc2[i] : rc[i];
-                            promote<C::CH, QVEC>(acc + c * C::CH, d, f, cv + i * BN + c * C::CH);
+                        };
+                        if constexpr (C::FRAG) {
+                            // Chunk c: rows 0 - 15 (c even) or 16 - 31 of the warp, 32 columns from 32 (c / 2).
+                            // The next chunk's read and factors go out before this one's additions.
+                            const float *cols = cv + i * BN + (lane & 3) * 2;
+                            const float *rows = sPv + (slot * SG + i) * BP + q4 * 32 + lane / 4;
+                            const float r[4] = {rows[0], rows[8], rows[16], rows[24]};
+                            float2 w[4];
+                            float f[2][16];
+                            uint32_t d[2][16];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float2 *>(cols + 8 * k);
+                            tmem_ld_16x256b_x4(ta + b * BN, d[0]);
+                            frag_factors(f[0], r, w);
+#pragma unroll
+                            for (int c = 0; c < C::NCH; ++c) {
+                                const int n = c + 1;
+                                tmem_landed<16>(d[c & 1]);
+                                if (n < C::NCH) {
+                                    if (n % 2 == 0) {
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+                                            w[k] = *reinterpret_cast<const float2 *>(cols + n / 2 * 32 + 8 * k);
+                                    }
+                                    tmem_ld_16x256b_x4(ta + ((uint32_t)(n & 1) << 20) + b * BN + n / 2 * 32, d[n & 1]);
+                                    frag_factors(f[n & 1], r + (n & 1) * 2, w);
+                                } else {
+                                    release();
+                                }
+#pragma unroll
+                                for (int k = 0; k < 16; k += 2)
+                                    fma2(acc[c * 16 + k], acc[c * 16 + k + 1], bits_f(d[c & 1][k]),
+                                         bits_f(d[c & 1][k + 1]), f[c & 1][k], f[c & 1][k + 1]);
+                            }
+                        } else {
+                            // One chunk in flight for each warp: the two warps of a scheduler take turns at
+                            // reading and adding.
+#pragma unroll
+                            for (int c = 0; c < C::NCH; ++c) {
+                                uint32_t d[C::CH];
+                                tmem_ld_32x32b_x16(ta + b * BN + c * C::CH, d);
+                                tmem_landed<C::CH>(d);
+                                if (c + 1 == C::NCH) release();
+                                const float f = C::TWO_BLOCKS && !VECB && c * C::CH >= turn ? rc2[i] : rc[i];
+                                promote<C::CH, QVEC>(acc + c * C::CH, d, f, cv + i * BN + c * C::CH);
+                            }
                         }
                     }
                 }
@@ -594,6 +660,12 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 if (SWAP) {
 #pragma unroll
                     for (int j = 0; j < C::ACC; ++j) st[(c0 + j) * (BP + 4) + prow] = acc[j];
+                } else if (C::FRAG) {
+#pragma unroll
+                    for (int j = 0; j < C::ACC; j += 2)
+                        *reinterpret_cast<float2 *>(st + (q4 * 32 + (j >> 1 & 1) * 8 + (j >> 4 & 1) * 16 + lane / 4) * (BN + 4) +
+                                                    c0 + j / 32 * 32 + j % 16 / 4 * 8 + (lane & 3) * 2) =
+                            make_float2(acc[j], acc[j + 1]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < C::ACC; j += 4)
@@ -622,7 +694,13 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                         sb[j + lane] = q0 + j + lane < g.Q ? bias_of(g, q0 + j + lane) : 0.0f;
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < C::ACC; j += 4) {
+                    for (int j = 0; j < C::ACC && C::FRAG; j += 2) {
+                        const float2 v = *reinterpret_cast<const float2 *>(sb + j / 32 * 32 + j % 16 / 4 * 8 + (lane & 3) * 2);
+                        acc[j] += v.x;
+                        acc[j + 1] += v.y;
+                    }
+#pragma unroll
+                    for (int j = 0; j < C::ACC && !C::FRAG; j += 4) {
                         const float4 v = *reinterpret_cast<const float4 *>(sb + j);
                         acc[j] += v.x;
                         acc[j + 1] += v.y;
@@ -631,9 +709,9 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     }
                 }
                 if (g.out_f32)
-                    store_rows<C::ACC, 16, true>(g, st, acc, lane, r0, q0);
+                    store_rows<C::ACC, 16, true, C::FRAG>(g, st, acc, lane, r0, q0);
                 else
-                    store_rows<C::ACC, 32, false>(g, st, acc, lane, r0, q0);
+                    store_rows<C::ACC, 32, false, C::FRAG>(g, st, acc, lane, r0, q0);
             }
         }
         __syncwarp();
@@ -821,9 +899,9 @@ hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
     const int64_t small = f8::blocks_of(c.M) * f8::blocks_of(c.N), rows2 = (c.M + 255) / 256;
     const int64_t mid = rows2 * ((c.N + 191) / 192), wide = rows2 * ((c.N + 255) / 256);
     const int64_t share = small * 2 > sms ? 1 : sms / small < 8 ? sms / small : 8;
-    const int64_t t_small = (small + sms - 1) / sms * (units / share * (VECB ? 455 : 290) + 1500);
-    const int64_t t_mid = (mid + pairs - 1) / pairs * (units * (VECB ? 640 : 415) + 1900);
-    const int64_t t_wide = (wide + pairs - 1) / pairs * (units * (VECB ? 830 : 475) + 2200);
+    const int64_t t_small = (small + sms - 1) / sms * (units / share * (VECB ? 420 : 290) + 1500);
+    const int64_t t_mid = (mid + pairs - 1) / pairs * (units * (VECB ? 580 : 415) + 1900);
+    const int64_t t_wide = (wide + pairs - 1) / pairs * (units * (VECB ? 715 : 475) + 2200);
     if (t_small <= t_mid && t_small <= t_wide) return launch<128, false, VECB, false>(c, g, s);
     if (t_mid < t_wide) return launch<192, false, VECB, true>(c, g, s);
     return launch<256, false, VECB, true>(c, g, s);
