@@ -16,7 +16,7 @@
 // by side on two granules each 262 us; next row prefetched in registers 263 us.
 // FP8 output 250 us, 0.55: bound by issue slots and the longer chain of a row
 // (about 630 instructions per warp and row), still less than the norm and the
-// quantizer one after the other (345 us).  Backward 335 us, 0.81 (two granules
+// quantizer one after the other (345 us).  Backward 336 us, 0.80 (two granules
 // a thread; with four its 200 registers leave one CTA per SM: 495 us).
 //
 // A thread fetches its own granules up to three rows ahead with cp.async into
@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 160 ? 3 :
     if (bad) status_or(a.status, HIF4_FLAG_NONFINITE);
 }
 
-template <bool XB, int V, int LANES, int WIDE>
+// TAIL: the row may end inside a granule.
+template <bool XB, int V, int LANES, int WIDE, bool TAIL = true>
 __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 && XB ? 2 : 1) k_norm_bwd(NormBwdArgs a)
 {
     constexpr int kDepth = depth<XB>(WIDE, V, 2), P = pieces<XB>(), ESZ = XB ? 2 : 4;
@@ -448,8 +449,14 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 && XB
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int n = in ? valid[v] : 0;
-            fetch8<XB>(ring + (stage * 2 * V + v) * P * nt, nt,
-                       n > 0 ? xs + v * T * 8 * ESZ : static_cast<const uint8_t *>(a.x), n);
+            const uint8_t *from = xs + v * T * 8 * ESZ;
+            int nx = n;
+            if (!TAIL && valid[v] == 0) {
+                // x past the row is the row's first granule: w is 0 there, and xh must be finite if the row's is
+                from = xs - t * 8 * ESZ;
+                nx = in ? 8 : 0;
+            }
+            fetch8<XB>(ring + (stage * 2 * V + v) * P * nt, nt, nx > 0 ? from : static_cast<const uint8_t *>(a.x), nx);
             fetch8<XB>(ring + (stage * 2 * V + V + v) * P * nt, nt,
                        n > 0 ? ds + v * T * 8 * ESZ : static_cast<const uint8_t *>(a.dy), n);
         }
@@ -489,8 +496,17 @@ __global__ void __launch_bounds__(WIDE ? WIDE : kSmallThreads, WIDE == 320 && XB
             widen8<XB>(fetched8<XB>(ring + (stage * 2 * V + v) * P * nt, nt), xh[v]);
             widen8<XB>(fetched8<XB>(ring + (stage * 2 * V + V + v) * P * nt, nt), d);
 #pragma unroll
+            for (int i = 0; i < 4; ++i) xh[v][i] = mul2(add2(xh[v][i], neg), r2);
+            if (TAIL && valid[v] < 8) {
+                // past the row x is 0 here, and xh may be infinite: 0 times it would be NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = unpack2(xh[v][i]);
+                    xh[v][i] = pack2(2 * i < valid[v] ? e.x : 0.0f, 2 * i + 1 < valid[v] ? e.y : 0.0f);
+                }
+            }
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
-                xh[v][i] = mul2(add2(xh[v][i], neg), r2);
                 dg[v][i] = fma2(d[i], xh[v][i], dg[v][i]);
                 db[v][i] = add2(db[v][i], d[i]);
                 w[v][i] = mul2(d[i], gm[v][i]);
@@ -648,7 +664,11 @@ template <bool XB>
 hif4_status launch_bwd(const NormBwdArgs &a, float *dgamma, float *dbeta, cudaStream_t s)
 {
     const Shape sh = shape_of(a.cols, 2);
-    void (*k)(NormBwdArgs) = sh.wide == 320 ? k_norm_bwd<XB, 2, 32, 320>
+    // Rows of whole granules have a variant without the test for what lies past them where registers are
+    // short: 57600 x 5120 BF16 336 us without, 382 with it; no difference in the other shapes.
+    const bool whole = a.cols % 8 == 0;
+    void (*k)(NormBwdArgs) = sh.wide == 320 && whole ? k_norm_bwd<XB, 2, 32, 320, false>
+                             : sh.wide == 320 ? k_norm_bwd<XB, 2, 32, 320>
                              : sh.wide == 512 ? k_norm_bwd<XB, 2, 32, 512>
                              : sh.wide ? k_norm_bwd<XB, 2, 32, 1024>
                              : sh.lanes == 8 ? k_norm_bwd<XB, 1, 8, 0>

@@ -118,6 +118,23 @@ def test_every_row_width_class(H, dt):  # noqa: F811
         R.assert_within(host(db), wb, e_db, "dbeta %d" % cols)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [3, 8, 60, 264, 517, 1300, 2880, 5112, 5121, 8200])
+def test_backward_of_rows_of_one_large_value(H, cols, dt):  # noqa: F811
+    """mean * rstd past the largest finite number: nothing of what lies past a row reaches its sums."""
+    import torch
+    rng = np.random.default_rng(cols)
+    x = on_gpu(np.full((5, cols), 2.0 ** 119), dtype_of(dt))
+    dy = on_gpu(rng.standard_normal((5, cols)), dtype_of(dt))
+    g, _ = params(rng, cols, "f32")
+    mean, rstd = torch.full((5,), 2.0 ** 119, device="cuda"), torch.full((5,), 1024.0, device="cuda")
+    dx, dg, db = H.layer_norm_backward(dy, x, mean, rstd, g)
+    want, wg, wb, e_dx, e_dg, e_db = R.norm_backward(host(dy), host(x), host(mean), host(rstd), num(g))
+    R.assert_within(host(dx), want, R.stored(e_dx, want, dt), "dx")
+    R.assert_within(host(dg), wg, e_dg, "dgamma")
+    R.assert_within(host(db), wb, e_db, "dbeta")
+
+
 @pytest.mark.parametrize("cols", [24, 200, 1300])
 def test_gradients_against_differences(H, cols):  # noqa: F811
     """Directional derivatives of L = sum(c y) by central differences of the 64-bit form."""
