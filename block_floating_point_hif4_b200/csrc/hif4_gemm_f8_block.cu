@@ -426,13 +426,19 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             }
             // Whether the tiles are done or a wait gave up: the copies land before the block leaves, and so do
             // the issuing CTA's arrivals on a second CTA's barriers (whose copies complete on the issuing
-            // CTA's).  Neither wait looks at the abort flag: after a time-out the MMA warps may still issue a
-            // unit that the promotion warps' last hand-off lets through, and its arrivals come late.
-            for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
-                const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
-                const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-                if (!PAIR || rank == 0) mbar_wait_bounded(&full[s], ph, nullptr, DRAIN_NS);
-                if (PAIR) mbar_wait_bounded(&empty[s], ph, nullptr, DRAIN_NS);
+            // CTA's).  Once a wait has given up, the MMA warps may still issue a unit that the promotion warps'
+            // last hand-off lets through, and its arrivals come late: all are waited for again then, whatever
+            // the abort flag says.
+            bool late = false;
+            for (int pass = 0; pass == 0 || (pass == 1 && late); ++pass) {
+                volatile uint32_t *flag = pass ? nullptr : abort_flag;
+                const uint64_t limit = pass ? DRAIN_NS : g.timeout_ns;
+                for (uint32_t i = 0; i < C::STAGES && i < issued && (pass || !late); ++i) {
+                    const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
+                    const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
+                    if (!PAIR || rank == 0) late |= !mbar_wait_bounded(&full[s], ph, flag, limit);
+                    if (PAIR) late |= !mbar_wait_bounded(&empty[s], ph, flag, limit);
+                }
             }
         } else if (warp == 3) {
             // ---------------------------------------------------- scales
