@@ -42,10 +42,15 @@
 // reads as well 2352, so about a fifth of the energy is the promotion, which
 // the FP32 scales cost.  A 128 x 256 tile of one CTA measured 3 to 8 % slower.
 //
+// A unit's MMAs announce their completion once, on the barrier of the stage
+// they read (in both CTAs of a pair): it hands the stage back to the producer
+// and the accumulator to the promotion warps.
+//
 // Every mbarrier wait is bounded (4 s); a role that gives up sets the block's
-// abort flag, the producers let their copies land and the arrivals of a pair's
-// other CTA come in, the MMA warps drain their MMAs before TMEM is freed, every
-// thread still meets the cluster barriers, and HIF4_FLAG_TIMEOUT is raised.
+// abort flag, the MMA warps drain their MMAs, the producers wait until those
+// warps have left and then for every copy and every completion still under way
+// (in a pair some of them arrive from the other CTA), every thread still meets
+// the cluster barriers, and HIF4_FLAG_TIMEOUT is raised.
 #include <mutex>
 
 #include "hif4_f8.cuh"
@@ -91,7 +96,7 @@ struct Cfg {
     static constexpr int RING = STAGES * (P_BYTES + Q_BYTES);
     static constexpr int TMEM_COLS = BN > 128 ? 512 : 2 * BN;         // a power of two
     static constexpr bool TWO_BLOCKS = BN == 192;                     // a thread's columns lie in up to two blocks of b
-    static constexpr int BARS = 2 * STAGES + 4 + 2 + 2 * SLOTS;
+    static constexpr int BARS = 2 * STAGES + 2 + 2 + 2 * SLOTS;
     static constexpr bool PVEC = !SWAP || VECB, QVEC = SWAP || VECB;  // P / Q carry scale vectors
     static constexpr int PV = PVEC ? SLOTS * SG * BP : 0, QV = QVEC ? SLOTS * SG * BN : 0;
     static constexpr int STORE = SWAP ? 0 : EPI_WARPS * ST_BYTES;
@@ -331,9 +336,8 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     float *sPv = reinterpret_cast<float *>(sSt + C::STORE);               // [SLOTS][SG][BP]
     float *sQv = sPv + C::PV;                                             // [SLOTS][SG][BN]
     uint64_t *full = reinterpret_cast<uint64_t *>(sQv + C::QV);
-    uint64_t *empty = full + C::STAGES;
-    uint64_t *tfull = empty + C::STAGES;
-    uint64_t *tempty = tfull + 2;
+    uint64_t *done = full + C::STAGES;                                    // the MMAs that read a stage have completed
+    uint64_t *tempty = done + C::STAGES;
     uint64_t *drain = tempty + 2;
     uint64_t *sfull = drain + 2;
     uint64_t *sempty = sfull + SLOTS;
@@ -346,10 +350,9 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&done[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
-            mbar_init(&tfull[a], 1);
             mbar_init(&tempty[a], C::EPI_WARPS * (PAIR ? 2 : 1));
             mbar_init(&drain[a], 1);
         }
@@ -397,7 +400,7 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 tile_coords(t, g, pb, qb);
                 const int prow = (pb * p_of + p_at) * BP, qrow = qb * BN + (PAIR ? rank * (BN / 2) : 0);
                 for (int u = u0; u < u1; ++u) {
-                    if (!mbar_wait_spin(&empty[stage], phase ^ 1u, abort_flag, g.timeout_ns)) {
+                    if (!mbar_wait_spin(&done[stage], phase ^ 1u, abort_flag, g.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -424,22 +427,24 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     }
                 }
             }
-            // Whether the tiles are done or a wait gave up: the copies land before the block leaves, and so do
-            // the issuing CTA's arrivals on a second CTA's barriers (whose copies complete on the issuing
-            // CTA's).  Once a wait has given up, the MMA warps may still issue a unit that the promotion warps'
-            // last hand-off lets through, and its arrivals come late: all are waited for again then, whatever
-            // the abort flag says.
-            bool late = false;
-            for (int pass = 0; pass == 0 || (pass == 1 && late); ++pass) {
-                volatile uint32_t *flag = pass ? nullptr : abort_flag;
-                const uint64_t limit = pass ? DRAIN_NS : g.timeout_ns;
-                for (uint32_t i = 0; i < C::STAGES && i < issued && (pass || !late); ++i) {
+            // Whether the tiles are done or a wait gave up: the copies land before the block leaves (a pair's all
+            // complete on the issuing CTA's barriers), and so do the completions of the MMAs.
+            const auto landed = [&](volatile uint32_t *flag, uint64_t limit) {
+                bool all = true;
+                for (uint32_t i = 0; i < C::STAGES && i < issued && (all || !flag); ++i) {
                     const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
                     const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-                    if (!PAIR || rank == 0) late |= !mbar_wait_bounded(&full[s], ph, flag, limit);
-                    if (PAIR) late |= !mbar_wait_bounded(&empty[s], ph, flag, limit);
+                    if (!PAIR || rank == 0) all &= mbar_wait_bounded(&full[s], ph, flag, limit);
+                    all &= mbar_wait_bounded(&done[s], ph, flag, limit);
                 }
-            }
+                return all;
+            };
+            const bool all = landed(abort_flag, g.timeout_ns);
+            // Once a wait has given up, the MMA warps may still issue a unit that the promotion warps' last
+            // hand-off lets through.  Their drain says that they have left, not that every completion that they
+            // asked for has arrived, so those are waited for again then, whatever the abort flag says.
+            for (int b = 0; b < 2; ++b) mbar_wait_bounded(&drain[b], 0, nullptr, 2 * g.timeout_ns + DRAIN_NS);
+            if (!all) landed(nullptr, DRAIN_NS);
         } else if (warp == 3) {
             // ---------------------------------------------------- scales
             // A slot holds those of SG consecutive units of a tile (the last one of a tile maybe fewer).
@@ -504,14 +509,12 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
 #pragma unroll
                                 for (int k = 0; k < KU / 32; ++k)
                                     mma_f8f6f4_pair(d, pd + 2 * k, qd + 2 * k, g.idesc, k > 0);
-                                mma_commit_pair(&tfull[b]);
-                                mma_commit_pair(&empty[stage]);
+                                mma_commit_pair(&done[stage]);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < KU / 32; ++k)
                                     mma_f8f6f4(d, pd + 2 * k, qd + 2 * k, g.idesc, k > 0);
-                                mma_commit(&tfull[b]);
-                                mma_commit(&empty[stage]);
+                                mma_commit(&done[stage]);
                             }
                         }
                         __syncwarp();
@@ -525,7 +528,7 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             // no MMA may still be running when TMEM is released
             if (elect_one()) {
                 if (PAIR)
-                    mma_commit_pair_local(&drain[b]);
+                    mma_commit_pair(&drain[b]);
                 else
                     mma_commit(&drain[b]);
             }
@@ -545,7 +548,9 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         const int c0 = (warp / 4 - 1) * C::ACC;          // and its first column
         const uint32_t ta = tmem_base + ((uint32_t)(q4 * 32) << 16) + c0;
         const uint32_t rel = PAIR ? peer_addr(smem_addr(tempty), 0) : smem_addr(tempty);   // of the issuing CTA
-        uint32_t slot = 0, sphase = 0, tph0 = 0, tph1 = 0;
+        // Unit by unit through the stages' completions.  None is missed: a stage is read again only by a unit
+        // STAGES later, and that one waits for an accumulator that a unit after this one has left.
+        uint32_t slot = 0, sphase = 0, stage = 0, phase = 0;
         bool ok = true;
         for (int t = t0; ok && t < g.num_tiles; t += tstep) {
             int pb, qb;
@@ -583,10 +588,12 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     if (u + i < u1) {
                         constexpr int odd[4] = {0, 1, 0, 1};
                         const uint32_t b = odd[i & 3];
-                        uint32_t &tph = b ? tph1 : tph0;
                         // (after a time-out the group is finished on whatever lies there, and then left)
-                        ok &= mbar_wait_spin(&tfull[b], tph, abort_flag, g.timeout_ns);
-                        tph ^= 1u;
+                        ok &= mbar_wait_spin(&done[stage], phase, abort_flag, g.timeout_ns);
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                         tc_fence_after();
                         // the accumulator is free once its last read has landed
                         const auto release = [&] {

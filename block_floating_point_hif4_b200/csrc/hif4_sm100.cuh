@@ -233,14 +233,6 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
         : "memory");
 }
 
-// Arrives once on this CTA's barrier when the pair's MMAs issued by this
-// thread have completed.
-__device__ __forceinline__ void mma_commit_pair_local(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
 // Address of the same shared-memory location in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
 {
