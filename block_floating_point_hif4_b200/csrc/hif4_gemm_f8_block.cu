@@ -88,9 +88,10 @@ struct Cfg {
     static constexpr int NCH = ACC / CH;
     static constexpr bool FRAG = VECB && !SWAP; // a thread's totals are those of 4 rows, not of one
     // registers: the promotion warps take what the producer's warpgroup gives back; the shares add up to
-    // what the launch brings along, 384 threads x 168
-    static constexpr int REG_LOW = BN >= 192 ? 72 : 0;
-    static constexpr int REG_HIGH = BN >= 192 ? 216 : 0;
+    // what the launch brings along, 384 threads x 168, or less (a scale per row of b: with 72 and 216 the
+    // compiler spills 60 bytes, with 96 and 200 24: 5120 x 5120 x 14391 577 -> 572 us)
+    static constexpr int REG_LOW = BN < 192 ? 0 : VECB ? 96 : 72;
+    static constexpr int REG_HIGH = BN < 192 ? 0 : VECB ? 200 : 216;
     static constexpr int P_BYTES = BP * KU;
     static constexpr int Q_BYTES = BN * KU / (PAIR ? 2 : 1);
     static constexpr int RING = STAGES * (P_BYTES + Q_BYTES);
@@ -393,7 +394,8 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         reg_dec<C::REG_LOW>();
         if (warp == 0) {
             // ---------------------------------------------------- operands
-            uint32_t stage = 0, phase = 0, issued = 0;
+            uint32_t stage = 0, phase = 0;
+            int issued = 0;
             bool ok = true;
             for (int t = t0; ok && t < g.num_tiles; t += tstep) {
                 int pb, qb;
@@ -429,21 +431,23 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             }
             // Whether the tiles are done or a wait gave up: the copies land before the block leaves (a pair's all
             // complete on the issuing CTA's barriers), and so do the completions of the MMAs.
+            // Each lane waits for a stage.
+            const uint32_t mine = (stage + C::STAGES - 1 - lane % C::STAGES) % C::STAGES;
+            const uint32_t ph = (mine < stage) ? phase : (phase ^ 1u);
             const auto landed = [&](volatile uint32_t *flag, uint64_t limit) {
                 bool all = true;
-                for (uint32_t i = 0; i < C::STAGES && i < issued && (all || !flag); ++i) {
-                    const uint32_t s = (stage + C::STAGES - 1 - i) % C::STAGES;
-                    const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-                    if (!PAIR || rank == 0) all &= mbar_wait_bounded(&full[s], ph, flag, limit);
-                    all &= mbar_wait_bounded(&done[s], ph, flag, limit);
+                if (lane < C::STAGES && lane < issued) {
+                    if (!PAIR || rank == 0) all = mbar_wait_bounded(&full[mine], ph, flag, limit);
+                    if (all || !flag) all &= mbar_wait_bounded(&done[mine], ph, flag, limit);
                 }
-                return all;
+                return __all_sync(0xFFFFFFFFu, all) != 0;
             };
             const bool all = landed(abort_flag, g.timeout_ns);
             // Once a wait has given up, the MMA warps may still issue a unit that the promotion warps' last
             // hand-off lets through.  Their drain says that they have left, not that every completion that they
             // asked for has arrived, so those are waited for again then, whatever the abort flag says.
-            for (int b = 0; b < 2; ++b) mbar_wait_bounded(&drain[b], 0, nullptr, 2 * g.timeout_ns + DRAIN_NS);
+            if (lane < 2) mbar_wait_bounded(&drain[lane], 0, nullptr, 2 * g.timeout_ns + DRAIN_NS);
+            __syncwarp();
             if (!all) landed(nullptr, DRAIN_NS);
         } else if (warp == 3) {
             // ---------------------------------------------------- scales
