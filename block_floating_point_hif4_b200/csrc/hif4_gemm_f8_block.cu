@@ -458,22 +458,37 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 int pb, qb;
                 tile_coords(t, g, pb, qb);
                 const int prow = (pb * p_of + p_at) * BP, qrow = qb * BN;
-                // (a pair's second CTA may lie past the last row; it then has nothing to read)
-                const int pn = max(0, min(BP, (g.P - prow + 3) & ~3)), qn = min(BN, (g.Q - qrow + 3) & ~3);
+                // scales of the tile's rows (a pair's second CTA may lie past the last row: none): whole 16-byte
+                // pieces by bulk copy, the last 1 to 3 one by one, so that nothing past the last row is read
+                const int pn = PVEC ? max(0, min(BP, g.P - prow)) : 0, qn = QVEC ? min(BN, g.Q - qrow) : 0;
+                const int pw = pn & ~3, qw = qn & ~3;
                 for (int u = u0; u < u1; u += SG) {
                     if (!mbar_wait_spin(&sempty[slot], phase ^ 1u, abort_flag, g.timeout_ns)) {
                         ok = false;
                         break;
                     }
+                    const int n = min(SG, u1 - u);
+                    if ((pn | qn) & 3) {                // lane = 8 x unit + 4 x operand + scale
+                        const int i = lane >> 3, k = lane & 3;
+                        const bool q = lane & 4;
+                        if (i < n && k < ((q ? qn : pn) & 3)) {
+                            if (q)
+                                async_load4(sQv + (slot * SG + i) * BN + qw + k, g.q_vec + (u + i) * g.q_ld + qrow + qw + k,
+                                            &sfull[slot]);
+                            else
+                                async_load4(sPv + (slot * SG + i) * BP + pw + k, g.p_vec + (u + i) * g.p_ld + prow + pw + k,
+                                            &sfull[slot]);
+                        }
+                        __syncwarp();
+                    }
                     if (elect_one()) {
-                        const int n = min(SG, u1 - u);
-                        mbar_arrive_expect_tx(&sfull[slot], (uint32_t)(n * ((PVEC ? pn : 0) + (QVEC ? qn : 0)) * 4));
+                        mbar_arrive_expect_tx(&sfull[slot], (uint32_t)(n * (pw + qw) * 4));
                         for (int i = 0; i < n; ++i) {
-                            if (PVEC && pn > 0)
-                                bulk_load(sPv + (slot * SG + i) * BP, g.p_vec + (u + i) * g.p_ld + prow, pn * 4,
+                            if (PVEC && pw > 0)
+                                bulk_load(sPv + (slot * SG + i) * BP, g.p_vec + (u + i) * g.p_ld + prow, pw * 4,
                                           &sfull[slot]);
-                            if (QVEC)
-                                bulk_load(sQv + (slot * SG + i) * BN, g.q_vec + (u + i) * g.q_ld + qrow, qn * 4,
+                            if (QVEC && qw > 0)
+                                bulk_load(sQv + (slot * SG + i) * BN, g.q_vec + (u + i) * g.q_ld + qrow, qw * 4,
                                           &sfull[slot]);
                         }
                     }

@@ -291,8 +291,8 @@ hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t rows, int6
  * b     N x K codes (b_fmt, ldb), sb by b_block_rows: 128 = 128 x 128 blocks
  *       (lds_b >= ceil(K / 128)), 1 = 1 x 128 blocks (lds_b >= N).
  * The block-major scale arrays are 16-byte aligned, their leading dimensions
- * multiples of 4 (they are read in 16-byte pieces; what lies between M or N
- * and the next multiple of 4 never reaches y).
+ * multiples of 4 (they are read in 16-byte pieces, the last 1 to 3 scales of a
+ * row one by one: nothing behind M or N is read, in the last row either).
  * bias  NULL or BF16 [N].   y  BF16 (FP32 with HIF4_LINEAR_OUT_F32, the only
  *       flag) M x N, ldy.
  * For up to 32 rows of a the weight is streamed once, K split over a cluster
