@@ -53,6 +53,8 @@
 // the cluster barriers, and HIF4_FLAG_TIMEOUT is raised.
 #include <mutex>
 
+#include <cuda_fp16.h>
+
 #include "hif4_f8.cuh"
 #include "hif4_pdl.cuh"
 #include "hif4_sm100.cuh"
@@ -70,6 +72,7 @@ constexpr int SG = 4;                           // units per slot of the scale r
 constexpr int SLOTS = 2;
 constexpr int ST_BYTES = 2048;                 // a promotion warp's staging of its stores: 32 rows of 64 bytes
 constexpr int GROUP = 16;                       // raster: P tiles per group
+constexpr float FLT_TOP = 3.402823466e38f;
 constexpr uint64_t TIMEOUT_NS = 4000000000ull;
 constexpr uint64_t DRAIN_NS = 20000000ull;
 
@@ -88,10 +91,10 @@ struct Cfg {
     static constexpr int NCH = ACC / CH;
     static constexpr bool FRAG = VECB && !SWAP; // a thread's totals are those of 4 rows, not of one
     // registers: the promotion warps take what the producer's warpgroup gives back; the shares add up to
-    // what the launch brings along, 384 threads x 168, or less (a scale per row of b: with 72 and 216 the
-    // compiler spills 60 bytes, with 96 and 200 24: 5120 x 5120 x 14391 577 -> 572 us)
-    static constexpr int REG_LOW = BN < 192 ? 0 : VECB ? 96 : 72;
-    static constexpr int REG_HIGH = BN < 192 ? 0 : VECB ? 200 : 216;
+    // what the launch brings along, 384 threads x 168, or less (192 columns with a scale per row of b: 69 us
+    // with 96 and 200, 74 with 72 and 216, 512 x 5120 x 13824; 256 columns: 589 and 577, 5120 x 5120 x 14391)
+    static constexpr int REG_LOW = BN < 192 ? 0 : VECB && BN == 192 ? 96 : 72;
+    static constexpr int REG_HIGH = BN < 192 ? 0 : VECB && BN == 192 ? 200 : 216;
     static constexpr int P_BYTES = BP * KU;
     static constexpr int Q_BYTES = BN * KU / (PAIR ? 2 : 1);
     static constexpr int RING = STAGES * (P_BYTES + Q_BYTES);
@@ -109,6 +112,10 @@ struct Cfg {
 
 struct Args {
     int P, Q;                                   // rows of the two operands
+    int K;
+    const uint8_t *p_codes, *q_codes;           // the operands again, for sum_again()
+    int64_t p_codes_ld, q_codes_ld;
+    uint32_t p_e5m2, q_e5m2;
     int num_p, num_q, num_u, num_tiles;
     int split;                                  // CTAs that share a tile's K (the cluster)
     const float *p_vec, *q_vec;                 // scale vectors [num_u][ld] (null: block scales)
@@ -322,9 +329,118 @@ __device__ __forceinline__ float bias_of(const Args &g, int n)
     return g.bias ? bits_f((uint32_t)__ldg(g.bias + n) << 16) : 0.0f;
 }
 
+// ---- Products of scales that overflow.  The tiles form sa sb first, one factor for an element's block sum (or for a
+// row's).  Where that is infinite although both scales are finite, the term can still be an ordinary number, or 0.  A CTA
+// that met such a product goes over its tiles once they are stored, and sums the elements concerned again, one by one.
+// It is seen on a row's factor, or, where each column has a factor of its own, on a total that is not finite.  Nothing of
+// it is in the loop over the units: a second form of that loop for large scales took 682 us instead of 597 (8192 x 13824
+// x 5120); with the warp that copies the scales looking at them it was 629 instead of 617, and 600 instead of 570 (5120 x
+// 5120 x 14391).  As it is: 618 instead of 617, and 586 instead of 576.
+
+// Values of two codes (the low byte first).
+__device__ __forceinline__ float2 code_values(uint32_t c, bool e5m2)
+{
+    uint32_t h;
+    if (e5m2)
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    else
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// sum a[k] b[k] over n codes (both 16-byte aligned)
+__device__ __forceinline__ float code_sum(const uint8_t *a, const uint8_t *b, int n, bool a_e5m2, bool b_e5m2)
+{
+    float sum = 0.0f;
+    int k = 0;
+    for (; k + 16 <= n; k += 16) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(a + k), w = *reinterpret_cast<const uint4 *>(b + k);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w}, y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 c = code_values(x[i >> 1] >> (16 * (i & 1)), a_e5m2);
+            const float2 d = code_values(y[i >> 1] >> (16 * (i & 1)), b_e5m2);
+            sum = fmaf(c.x, d.x, fmaf(c.y, d.y, sum));
+        }
+    }
+    for (; k < n; ++k) sum = fmaf(code_values(a[k], a_e5m2).x, code_values(b[k], b_e5m2).x, sum);
+    return sum;
+}
+
+// The scales of element (p, q) in unit u.
+__device__ __forceinline__ float2 scales_of(const Args &g, int64_t p, int64_t q, int u)
+{
+    return make_float2(g.p_vec ? g.p_vec[u * g.p_ld + p] : g.blk[p / 128 * g.blk_ld + u],
+                       g.q_vec ? g.q_vec[u * g.q_ld + q] : g.blk[q / 128 * g.blk_ld + u]);
+}
+
+__device__ __forceinline__ bool overflows(float2 s)
+{
+    return fabsf(s.x * s.y) > FLT_TOP && fabsf(s.x) <= FLT_TOP && fabsf(s.y) <= FLT_TOP;
+}
+
+// Whether row p has a scale that can be part of an overflow (the other one is finite).
+__device__ __forceinline__ bool may_overflow(const Args &g, int64_t p)
+{
+    bool may = false;
+    for (int u = 0; u < g.num_u; ++u) may |= fabsf(scales_of(g, p, 0, u).x) > 1.0f;
+    return may;
+}
+
+// The total of an element over all units, as if no product of scales could overflow; false if none does.
+__device__ __forceinline__ bool sum_again(const Args &g, int64_t p, int64_t q, float &total)
+{
+    int u = 0;
+    while (u < g.num_u && !overflows(scales_of(g, p, q, u))) ++u;
+    if (u == g.num_u) return false;
+    total = 0.0f;
+#pragma unroll 1
+    for (u = 0; u < g.num_u; ++u) {
+        float sum = code_sum(g.p_codes + p * g.p_codes_ld + u * KU, g.q_codes + q * g.q_codes_ld + u * KU,
+                             min(KU, g.K - u * KU), g.p_e5m2, g.q_e5m2);
+        const float2 s = scales_of(g, p, q, u);
+        float f = s.x * s.y;
+        if (overflows(s)) {
+            // Both are above 1.  2^40 goes from the one to the sum (below 2^40, and at least 2^-32 if not 0); what is
+            // too large even so meets a sum that takes it past the largest number anyway, or 0.
+            sum *= 1099511627776.0f;
+            f = fminf(fmaxf(s.x * (1.0f / 1099511627776.0f) * s.y, -FLT_TOP), FLT_TOP);
+        }
+        total = fmaf(sum, f, total);
+    }
+    return true;
+}
+
+template <bool SWAP>
+__device__ __forceinline__ void store_again(const Args &g, int64_t p, int64_t q)
+{
+    float v;
+    if (p < g.P && q < g.Q && sum_again(g, p, q, v)) {
+        const int n = (int)(SWAP ? p : q);
+        store_one(g, SWAP ? q : p, n, v + bias_of(g, n));
+    }
+}
+
+// All elements of a CTA's tiles.
+template <int BN, bool SWAP, bool PAIR>
+__device__ __forceinline__ void tiles_again(const Args &g, int t0, int tstep, int rank)
+{
+    for (int t = t0; t < g.num_tiles; t += tstep) {
+        int pb, qb;
+        tile_coords(t, g, pb, qb);
+        for (int i = threadIdx.x; i < BP * (BN / 16); i += blockDim.x) {            // 16 elements of a row
+            const int p = (PAIR ? pb * 2 + rank : pb) * BP + i % BP, q = qb * BN + i / BP * 16;
+            if (p < g.P && may_overflow(g, p))
+#pragma unroll 1
+                for (int j = 0; j < 16; ++j) store_again<SWAP>(g, p, q + j);
+        }
+    }
+}
+
 template <int BN, bool SWAP, bool VECB, bool PAIR>
 __global__ void __launch_bounds__(Cfg<BN, VECB, PAIR, SWAP>::THREADS, Cfg<BN, VECB, PAIR, SWAP>::CTAS)
-k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, Args g)
+k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                const __grid_constant__ Args g)
 {
     using namespace sm100;
     using C = Cfg<BN, VECB, PAIR, SWAP>;
@@ -344,6 +460,7 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     uint64_t *sempty = sfull + SLOTS;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sempty + SLOTS);
     volatile uint32_t *abort_flag = tmem_holder + 1;
+    volatile uint32_t *again = tmem_holder + 2;                           // a product of scales may have overflowed
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -362,10 +479,15 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             mbar_init(&sempty[s], C::EPI_WARPS);
         }
         *abort_flag = 0u;
+        *again = 0u;
         fence_barrier_init();
         prefetch_tensormap(&tmP);
         prefetch_tensormap(&tmQ);
     }
+    // Scales of rows past the last one are never copied: 0, so that nothing looks like an overflow there.
+    for (int i = threadIdx.x; i < (C::PV + C::QV) / 4; i += C::THREADS)
+        reinterpret_cast<float4 *>(sPv)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    fence_proxy_async();
     if (warp == 1) {
         if (PAIR) {
             tmem_alloc_pair(tmem_holder, C::TMEM_COLS);
@@ -674,6 +796,15 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     }
                 }
                 if (!ok) break;
+                if (!QVEC) {                            // (down here the factors have long arrived)
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < SG; ++i) {
+                        top = fmaxf(top, fabsf(rc[i]));
+                        if (C::TWO_BLOCKS) top = fmaxf(top, fabsf(rc2[i]));
+                    }
+                    if (top > FLT_TOP) *again = 1u;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[slot]);
                 if (++slot == SLOTS) {
@@ -684,6 +815,12 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             if (!ok) break;
             const int p = pb * BP + prow;
             const int q0 = qb * BN + c0;
+            if (QVEC) {
+                float z[4] = {};                        // 0 times a finite total is 0
+#pragma unroll
+                for (int j = 0; j < C::ACC; j += 2) fma2(z[j % 4], z[j % 4 + 1], acc[j], acc[j + 1], 0.0f, 0.0f);
+                if (!((z[0] + z[1]) + (z[2] + z[3]) == 0.0f)) *again = 1u;
+            }
             if (C::SPLITS && split > 1) {
                 // the last unit's MMAs have completed: nothing reads or writes the ring any more.
                 // Staged along y's contiguous axis, with a pitch that keeps 16-byte accesses free of
@@ -797,6 +934,7 @@ k_gemm_f8_block(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         else
             tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
+    if (*again && !*abort_flag) tiles_again<BN, SWAP, PAIR>(g, t0, tstep, rank);
     if (threadIdx.x == 0 && *abort_flag) status_or(g.status, HIF4_FLAG_TIMEOUT);
 }
 
@@ -850,6 +988,13 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
     g.num_p = (g.P + TP - 1) / TP;
     g.num_q = (g.Q + BN - 1) / BN;
     g.num_u = (int)f8::blocks_of(c.K);
+    g.K = (int)c.K;
+    g.p_codes = p;
+    g.q_codes = q;
+    g.p_codes_ld = SWAP ? c.ldb : c.lda;
+    g.q_codes_ld = SWAP ? c.lda : c.ldb;
+    g.p_e5m2 = SWAP ? c.b_e5m2 : c.a_e5m2;
+    g.q_e5m2 = SWAP ? c.a_e5m2 : c.b_e5m2;
     if ((int64_t)g.num_p * g.num_q > INT32_MAX / 8) return HIF4_ERR_UNSUPPORTED;
     g.num_tiles = g.num_p * g.num_q;
     g.p_vec = SWAP ? (VECB ? c.sb : nullptr) : c.sa;

@@ -123,6 +123,9 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *gsrc, uint
                  : "memory");
 }
 
+// Orders this thread's shared-memory accesses before later asynchronous (bulk, tensor) copies to the same places.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Four bytes global -> shared; `bar` waits for them too: its current phase, which must not be able to complete
 // before this call, expects one more arrival that comes when they have landed.
 __device__ __forceinline__ void async_load4(void *smem_dst, const void *gsrc, uint64_t *bar)

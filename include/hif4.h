@@ -283,10 +283,14 @@ hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t rows, int6
  *   y[m][n] = bias[n] + sum over blocks u of K of
  *             sa[u][m] sb[u, n] sum_{k in u} a[m][k] b[n][k]
  * on the FP8 tensor cores, FP32 accumulation, the scales applied in FP32 per
- * block, y rounded once.  Forward: a = activations, b = weight.  Input
- * gradient: a = output gradient, b = the transposed weight codes.  Weight
- * gradient: a, b = the transposed codes of the output gradient and of the
- * input, both with 1 x 128 blocks (b_block_rows = 1).
+ * block, y rounded once.  A block's sum meets the product sa sb rounded to
+ * FP32; one above the largest FP32 number counts as itself (a sum of 0 stays
+ * 0), one below 2^-126 is off by up to 2^-150.  Elements that meet the former
+ * are summed a second time, at the speed of scalar code.
+ * Forward: a = activations, b = weight.  Input gradient: a = output gradient,
+ * b = the transposed weight codes.  Weight gradient: a, b = the transposed
+ * codes of the output gradient and of the input, both with 1 x 128 blocks
+ * (b_block_rows = 1).
  * a     M x K codes (a_fmt, lda), sa 1 x 128 block scales (lds_a >= M).
  * b     N x K codes (b_fmt, ldb), sb by b_block_rows: 128 = 128 x 128 blocks
  *       (lds_b >= ceil(K / 128)), 1 = 1 x 128 blocks (lds_b >= N).
