@@ -1067,7 +1067,8 @@ hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
     if (c.M <= 32) return launch<32, true, VECB, false>(c, g, s);
     // 128 x 128 tiles of one CTA, or 256 x 192 or 256 x 256 tiles of a pair, by estimated time in ns: each
     // wave of tiles takes its units and its stores.  The larger a tile, the less a product costs in operand
-    // bytes and hand-offs; the smaller, the better the waves fill the SMs, and only the smallest share K.
+    // bytes and hand-offs; the smaller, the better the waves fill the SMs.  One wave of the smallest tiles is always
+    // chosen, since no larger tile takes less per unit; where it leaves half the SMs idle, they share K (launch).
     // Measured (us; 128 x 128 / 256 x 192 / 256 x 256): 128 x 5120 x 5120 12.9 / 19.5 / 23.4,
     // 512 x 5120 x 13824 68.3 / 50.6 / 57.8, 768 x 5120 x 13824 70.5 / 88.2 / 58.7, 1024 x 5120 x 5120
     // 40.4 / 38.3 / 44.6, 2048 x 13824 x 5120 165 / 147 / 142, 8192 x 5120 x 13824 628 / 575 / 544.
@@ -1075,8 +1076,7 @@ hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
     const int64_t units = f8::blocks_of(c.K), sms = sm_count(), pairs = sms / 2;
     const int64_t small = f8::blocks_of(c.M) * f8::blocks_of(c.N), rows2 = (c.M + 255) / 256;
     const int64_t mid = rows2 * ((c.N + 191) / 192), wide = rows2 * ((c.N + 255) / 256);
-    const int64_t share = small * 2 > sms ? 1 : sms / small < 8 ? sms / small : 8;
-    const int64_t t_small = (small + sms - 1) / sms * (units / share * (VECB ? 420 : 290) + 1500);
+    const int64_t t_small = (small + sms - 1) / sms * (units * (VECB ? 420 : 290) + 1500);
     const int64_t t_mid = (mid + pairs - 1) / pairs * (units * (VECB ? 580 : 415) + 1900);
     const int64_t t_wide = (wide + pairs - 1) / pairs * (units * (VECB ? 715 : 475) + 2200);
     if (t_small <= t_mid && t_small <= t_wide) return launch<128, false, VECB, false>(c, g, s);
