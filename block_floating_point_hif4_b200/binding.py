@@ -77,6 +77,7 @@ SIGNATURES = {
     "hif4_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P,
                                                 ctypes.c_int, _P, _I64, _P, _P, _P, _SZ, _P]),
     "hif4_debug_wait_test": (None, [ctypes.c_uint32, ctypes.c_uint64]),
+    "hif4_debug_gemm_f8_block_tiles": (ctypes.c_int, [_I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_int32)]),
     "hif4_get_status": (ctypes.c_int, [_P, _P]),
     "hif4_reset_status": (ctypes.c_int, [_P, _P]),
     "hif4_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -977,8 +977,9 @@ struct Call {
     bool a_e5m2, b_e5m2;
 };
 
+// tiles: not null to have the choice only (rows and columns of a tile, CTAs that share its K, CTAs).
 template <int BN, bool SWAP, bool VECB, bool PAIR>
-hif4_status launch(const Call &c, Args g, cudaStream_t stream)
+hif4_status launch(const Call &c, Args g, cudaStream_t stream, int32_t *tiles)
 {
     using CF = Cfg<BN, VECB, PAIR, SWAP>;
     const uint8_t *p = SWAP ? c.b : c.a, *q = SWAP ? c.a : c.b;
@@ -1006,12 +1007,6 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
     g.blk_rows = (int)f8::blocks_of(c.N);
     g.idesc = sm100::idesc_f8_f32(TP, BN, SWAP ? c.b_e5m2 : c.a_e5m2, SWAP ? c.a_e5m2 : c.b_e5m2);
 
-    CUtensorMap tmP, tmQ;
-    if (!make_tensor_map_u8_2d_sw128(&tmP, p, (uint64_t)c.K, (uint64_t)g.P, (uint64_t)(SWAP ? c.ldb : c.lda), KU,
-                                     BP) ||
-        !make_tensor_map_u8_2d_sw128(&tmQ, q, (uint64_t)c.K, (uint64_t)g.Q, (uint64_t)(SWAP ? c.lda : c.ldb), KU,
-                                     PAIR ? BN / 2 : BN))
-        return HIF4_ERR_UNSUPPORTED;            // the driver's encoder refused the layout
     auto k = k_gemm_f8_block<BN, SWAP, VECB, PAIR>;
     if (CF::REG_HIGH > 0) {
         // the promotion warps wait for registers that the launch must have brought along
@@ -1043,6 +1038,19 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
     int64_t grid = (int64_t)g.num_tiles * cluster;
     const int64_t slots = (int64_t)sm_count() * CF::CTAS / cluster * cluster;
     if (split == 1 && grid > slots) grid = slots;       // persistent
+    if (tiles) {
+        tiles[0] = TP;
+        tiles[1] = BN;
+        tiles[2] = split;
+        tiles[3] = (int32_t)grid;
+        return HIF4_OK;
+    }
+    CUtensorMap tmP, tmQ;
+    if (!make_tensor_map_u8_2d_sw128(&tmP, p, (uint64_t)c.K, (uint64_t)g.P, (uint64_t)(SWAP ? c.ldb : c.lda), KU,
+                                     BP) ||
+        !make_tensor_map_u8_2d_sw128(&tmQ, q, (uint64_t)c.K, (uint64_t)g.Q, (uint64_t)(SWAP ? c.lda : c.ldb), KU,
+                                     PAIR ? BN / 2 : BN))
+        return HIF4_ERR_UNSUPPORTED;            // the driver's encoder refused the layout
     cfg.gridDim = dim3((unsigned)grid);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1061,10 +1069,10 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream)
 }
 
 template <bool VECB>
-hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
+hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s, int32_t *tiles = nullptr)
 {
-    if (c.M <= 16) return launch<16, true, VECB, false>(c, g, s);
-    if (c.M <= 32) return launch<32, true, VECB, false>(c, g, s);
+    if (c.M <= 16) return launch<16, true, VECB, false>(c, g, s, tiles);
+    if (c.M <= 32) return launch<32, true, VECB, false>(c, g, s, tiles);
     // 128 x 128 tiles of one CTA, or 256 x 192 or 256 x 256 tiles of a pair, by estimated time in ns: each
     // wave of tiles takes its units and its stores.  The larger a tile, the less a product costs in operand
     // bytes and hand-offs; the smaller, the better the waves fill the SMs.  One wave of the smallest tiles is always
@@ -1079,9 +1087,9 @@ hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s)
     const int64_t t_small = (small + sms - 1) / sms * (units * (VECB ? 420 : 290) + 1500);
     const int64_t t_mid = (mid + pairs - 1) / pairs * (units * (VECB ? 580 : 415) + 1900);
     const int64_t t_wide = (wide + pairs - 1) / pairs * (units * (VECB ? 715 : 475) + 2200);
-    if (t_small <= t_mid && t_small <= t_wide) return launch<128, false, VECB, false>(c, g, s);
-    if (t_mid < t_wide) return launch<192, false, VECB, true>(c, g, s);
-    return launch<256, false, VECB, true>(c, g, s);
+    if (t_small <= t_mid && t_small <= t_wide) return launch<128, false, VECB, false>(c, g, s, tiles);
+    if (t_mid < t_wide) return launch<192, false, VECB, true>(c, g, s, tiles);
+    return launch<256, false, VECB, true>(c, g, s, tiles);
 }
 
 } // namespace gemm8b
@@ -1123,4 +1131,17 @@ extern "C" hif4_status hif4_gemm_f8_block(const uint8_t *a, hif4_f8_format a_fmt
     const Call c{a, b, M, N, K, lda, ldb, sa, sb, lds_a, lds_b, a_fmt == HIF4_E5M2, b_fmt == HIF4_E5M2};
     return vecb ? dispatch<true>(c, g, reinterpret_cast<cudaStream_t>(stream))
                 : dispatch<false>(c, g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" hif4_status hif4_debug_gemm_f8_block_tiles(int64_t M, int64_t N, int64_t K, int32_t b_block_rows,
+                                                      int32_t *tiles)
+{
+    if (M < 1 || N < 1 || K < 1 || (b_block_rows != 1 && b_block_rows != 128) || !tiles) return HIF4_ERR_INVALID_ARG;
+    if (M > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2) return HIF4_ERR_UNSUPPORTED;
+    gemm8b::Call c{};
+    c.M = M;
+    c.N = N;
+    c.K = K;
+    return b_block_rows == 1 ? gemm8b::dispatch<true>(c, gemm8b::Args{}, nullptr, tiles)
+                             : gemm8b::dispatch<false>(c, gemm8b::Args{}, nullptr, tiles);
 }

@@ -588,6 +588,15 @@ hif4_status hif4_ptq_state_unpack(const void *buf, size_t bytes, uint8_t *codes,
  */
 void hif4_debug_wait_test(uint32_t withhold, uint64_t limit_ns);
 
+/*
+ * hif4_debug_gemm_f8_block_tiles — the tiles that hif4_gemm_f8_block takes for
+ * these sizes on the current device, so that a test knows what it covers:
+ * tiles[0..3] (host memory) = rows and columns of a tile (the weight's rows
+ * first for up to 32 rows of a), the CTAs that share a tile's K, the CTAs of
+ * the launch.  Launches nothing.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+hif4_status hif4_debug_gemm_f8_block_tiles(int64_t M, int64_t N, int64_t K, int32_t b_block_rows, int32_t *tiles);
+
 /* Synchronizes `stream`, reads the device status word and maps its bits:
  * TIMEOUT -> HIF4_ERR_TIMEOUT, BAD_INDEX or NOT_SPD -> HIF4_ERR_INVALID_ARG,
  * NONFINITE -> HIF4_ERR_NONFINITE, none -> HIF4_OK.  The word is not cleared. */

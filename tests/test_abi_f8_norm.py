@@ -125,3 +125,11 @@ def test_layer_norm_backward_refusals(L):
     assert b(cols=16385, ldx=16392, lddx=16392, lddy=16392) == UNSUPPORTED
     assert b(cols=0) == 0
     assert b(rows=0, dg=None, db=None) == 0              # no sums wanted, no rows
+
+
+def test_tiles_of_a_product_refusals(L):
+    t = (ctypes.c_int32 * 4)()
+    f = L.hif4_debug_gemm_f8_block_tiles
+    assert f(0, 10, 10, 1, t) == INVALID and f(10, 0, 10, 1, t) == INVALID and f(10, 10, 0, 1, t) == INVALID
+    assert f(10, 10, 10, 2, t) == INVALID and f(10, 10, 10, 128, None) == INVALID
+    assert f(1 << 31, 10, 10, 1, t) == UNSUPPORTED
