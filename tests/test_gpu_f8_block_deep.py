@@ -5,11 +5,10 @@ takes is asked for and checked, so that a shape keeps testing what it is here fo
 The 64-bit products run on the GPU."""
 import ctypes
 
-import numpy as np
 import pytest
 
 from tests import _f8_ref as R
-from tests.test_gpu_f8_block import H, dtype_of, fmt_of  # noqa: F401
+from tests.test_gpu_f8_block import H, fmt_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
