@@ -466,6 +466,10 @@ def ptq_state_unpack(record: bytes, device=None):
 # These calls are short enough for their marshalling to count: pointers are
 # passed as integers, padded tensors are allocated as such, and no context is
 # entered where device and stream are the current ones.
+#
+# Like every call here they are outside autograd: results carry no graph, whether
+# or not an input requires a gradient.  A training step makes the backward calls
+# itself (gemm_f8_block on transposed codes, layer_norm_backward).
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 _F8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}

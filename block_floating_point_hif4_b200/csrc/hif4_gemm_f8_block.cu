@@ -11,8 +11,9 @@
 // product with a's.  There a thread holds four rows of a quarter of the columns
 // (16x256b reads) and not one row (32x32b): a scale read from shared memory
 // serves four rows, else those reads take longer than the MMAs (5120 x 5120 x
-// 14391: 592 us with one row per thread, 489 with four; without the scales'
-// reads and products, in a trial copy, 440).
+// 14391 on a cool card: 592 us with one row per thread, 489 with four, 440 in a
+// trial copy without the scales' reads and products; a call, with the clock that
+// the power cap leaves, takes 571 with four).
 //
 // Roles: warp 0 issues the TMA loads (128-byte swizzled operand tiles into a
 // ring), warps 1 and 2 the MMAs into two alternating accumulators, warp 3 the
@@ -20,9 +21,9 @@
 // warps 4 and up promote.  A tile is 128 rows of one operand (P) by BN rows of
 // the other (Q).
 //   SWAP (BN 16, 32; up to 32 rows of a): the weight is P, so that it fills the
-//     MMA's 128 rows, and the tokens are Q.  Two CTAs per SM stream the weight:
-//     1 x 13824 x 5120 in 15.9 us, 4.5 TB/s, of which about 4 us are launch,
-//     first load and stores.
+//     MMA's 128 rows, and the tokens are Q.  Up to two CTAs per SM stream the
+//     weight: 1 x 13824 x 5120 in 16.0 us, 4.4 TB/s, 5 of them before the first
+//     block starts or after the last has ended.
 //   128 x 128 tiles: short products of more rows.
 //   PAIR: 256 x 256 or 256 x 192 tiles of a cluster of two CTAs (tcgen05
 //     cta_group::2).  Each CTA loads 128 rows of P and half of Q's, 32 KB a unit
@@ -35,12 +36,15 @@
 // the CTAs in rank order (distributed shared memory).  The order of the sum is
 // fixed and no workspace is needed.
 //
-// What bounds the large products, measured at 57600 x 13824 x 5120: the 1 kW
-// power cap.  In a burst the pair kernel runs at 2157 TFLOP/s, sustained at
-// 1880 (1.53 GHz, about 1010 cycles a unit and pair of tiles); with the
-// promotion's FMAs left out in a trial copy it sustained 2126, without its TMEM
-// reads as well 2352, so about a fifth of the energy is the promotion, which
-// the FP32 scales cost.  A 128 x 256 tile of one CTA measured 3 to 8 % slower.
+// What bounds the large products, measured at 57600 x 13824 x 5120 in cycles of
+// the SM clock: a unit takes 930 cycles, whether in one launch (1.60 GHz, 3850 us)
+// or sustained (1.37 GHz, 4570 us), where its MMAs need 512.  The MMA warps wait
+// 1300 of the 1910 cycles between two units of theirs for a free accumulator and 85
+// for operands; a promotion warp waits 200 of 960 cycles for MMAs (trial copy with
+// clocks).  Without the promotion's FMAs a unit takes 650 cycles, without its TMEM
+// reads as well 644: the FMAs and the hand-off of the two accumulators are the
+// bound, and the 1 kW power cap then sets the clock.  Half of the operands' bytes
+// changes nothing (925).  A 128 x 256 tile of one CTA measured 3 to 8 % slower.
 //
 // A unit's MMAs announce their completion once, on the barrier of the stage
 // they read (in both CTAs of a pair): it hands the stage back to the producer
@@ -1029,7 +1033,8 @@ hif4_status launch(const Call &c, Args g, cudaStream_t stream, int32_t *tiles)
         // K is shared by as many CTAs as can all be resident at once, while each keeps at least 8 units:
         // with fewer, filling the ring and joining the parts costs more than it saves (1 x 5120 x 5120,
         // 40 units: 12.7 us on 1 CTA a tile, 9.4 on 2, 8.6 on 3 or 4, 8.8 on 5 or 6, 13.3 on 8, whose
-        // clusters no longer fit beside one another).
+        // clusters no longer fit beside one another).  The occupancy query counts one CTA to an SM for a kernel
+        // that allocates tensor memory, though two run where they fit: clusters stay within one.
         for (int s = 2; s <= 8 && g.num_u >= 8 * s && (int64_t)g.num_tiles * s <= (int64_t)sm_count() * CF::CTAS; ++s)
             if (resident_clusters(reinterpret_cast<const void *>(k), cfg, s) >= g.num_tiles) split = s;
     }
@@ -1077,7 +1082,8 @@ hif4_status dispatch(const Call &c, const Args &g, cudaStream_t s, int32_t *tile
     // wave of tiles takes its units and its stores.  The larger a tile, the less a product costs in operand
     // bytes and hand-offs; the smaller, the better the waves fill the SMs.  One wave of the smallest tiles is always
     // chosen, since no larger tile takes less per unit; where it leaves half the SMs idle, they share K (launch).
-    // Measured (us; 128 x 128 / 256 x 192 / 256 x 256): 128 x 5120 x 5120 12.9 / 19.5 / 23.4,
+    // Measured when the rule was set (us, device time; 128 x 128 / 256 x 192 / 256 x 256; the chosen ones have
+    // moved by -7 to +2 % since): 128 x 5120 x 5120 12.9 / 19.5 / 23.4,
     // 512 x 5120 x 13824 68.3 / 50.6 / 57.8, 768 x 5120 x 13824 70.5 / 88.2 / 58.7, 1024 x 5120 x 5120
     // 40.4 / 38.3 / 44.6, 2048 x 13824 x 5120 165 / 147 / 142, 8192 x 5120 x 13824 628 / 575 / 544.
     // A unit takes longer where b has a scale per row: two operations per element instead of one.

@@ -9,15 +9,24 @@
 // column sums, stay in registers for the life of a block, and a block takes
 // rows b, b + grid, ...
 //
-// Measured (device time): forward 57600 x 5120 BF16, FP32 parameters, with
-// statistics: 195 us, 6.05 TB/s, 0.92 of the copy bandwidth.  Four granules a
-// thread (160 threads a row, three CTAs per SM): with two (320 threads) 232 us,
+// Measured (device time in a loop; a call on cold operands takes 204 us for the
+// first): forward 57600 x 5120 BF16, FP32 parameters, with statistics: 195 to
+// 212 us by the card's state, 0.92 to 0.85 of the copy bandwidth.  Four granules
+// a thread (160 threads a row, three CTAs per SM): with two (320 threads) 232 us,
 // since a row's shuffles and reciprocal are paid once per warp; two rows side
 // by side on two granules each 262 us; next row prefetched in registers 263 us.
-// FP8 output 250 us, 0.55: bound by issue slots and the longer chain of a row
-// (about 630 instructions per warp and row), still less than the norm and the
-// quantizer one after the other (345 us).  Backward 336 us, 0.80 (two granules
-// a thread; with four its 200 registers leave one CTA per SM: 495 us).
+// FP8 output 250 us, 0.55, still less than the norm and the quantizer one after
+// the other (345 us): a row is one chain of dependent steps (statistics, maxima,
+// quotient, encoding; 560 instructions per warp and row against 425), which the
+// 15 warps of an SM do not hide.  Issue slots are not the bound: 56 % busy, the
+// plain norm's 54 %.  Backward 336 us, 0.80 (two granules a thread; with four
+// its 200 registers leave one CTA per SM: 495 us).
+//
+// Other widths, 16384 rows BF16, share of the copy bandwidth: forward 0.86 at
+// 5120 columns, 0.69 at 5128 (the class of up to 512 threads a row), 0.85 at
+// 8192, 0.77 at 12288, 0.81 at 16384; backward 0.72, 0.66, 0.82, 0.37, 0.36.
+// Past 8192 columns the backward kernel's rows have 1024 threads of 64 registers,
+// 48 of which gamma and the column sums want: it spills 528 bytes (568 for FP32).
 //
 // A thread fetches its own granules up to three rows ahead with cp.async into
 // its own places of shared memory: no barrier, no registers for data in flight,
@@ -170,8 +179,8 @@ __device__ __forceinline__ void group_maxs(float (&v)[N])
 }
 
 // ---- the rows in flight: `depth` stages of [piece][thread] 16-byte pieces, each
-// written and read by its thread alone.  Four stages (60 KB in flight per SM for
-// rows of 5120 BF16), fewer where wide rows leave no room.
+// written and read by its thread alone.  Four stages (three rows of 10 KB ahead in
+// each of three CTAs per SM for 5120 BF16), fewer where wide rows leave no room.
 template <bool BF16>
 constexpr int pieces() { return BF16 ? 1 : 2; }
 

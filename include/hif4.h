@@ -271,7 +271,8 @@ hif4_status hif4_gemm_f8(const uint8_t *a, int64_t M, int64_t K, int64_t lda, co
  * Padding (columns past cols, scales past rows) is left as it was.
  * Errors: INVALID_ARG (null pointers, sizes < 0, dtype, format, block_rows),
  *         SHAPE (leading dimensions), ALIGNMENT (x, ldx, q, qt and theirs 16
- *         bytes; scales 4), UNSUPPORTED (rows x ceil(cols / 128) >= 2^31).
+ *         bytes; scales 4), UNSUPPORTED (rows, cols or rows x ceil(cols / 128)
+ *         >= 2^31).
  */
 hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
                              hif4_f8_format fmt, int32_t block_rows, uint8_t *q, int64_t ldq, float *scale,
@@ -304,9 +305,10 @@ hif4_status hif4_quantize_f8(const void *x, hif4_dtype dtype, int64_t rows, int6
  * overlap an input.
  * A NaN code makes the outputs that it reaches NaN.
  * Errors: SHAPE (K == 0 with M, N > 0; leading dimensions), ALIGNMENT,
- *         INVALID_ARG, UNSUPPORTED (sizes, or a layout the driver's
- *         tensor-map encoder refuses).  Bounded waits raise
- *         HIF4_FLAG_TIMEOUT as hif4_gemm_bf16.
+ *         INVALID_ARG, UNSUPPORTED (M, N or K >= 2^30, 2^28 tiles or more, or a
+ *         layout the driver's tensor-map encoder refuses).  Bounded waits raise
+ *         HIF4_FLAG_TIMEOUT as hif4_gemm_bf16: y is then incomplete, and without
+ *         a status word nothing says so.
  */
 hif4_status hif4_gemm_f8_block(const uint8_t *a, hif4_f8_format a_fmt, int64_t M, int64_t K, int64_t lda,
                                const float *sa, int64_t lds_a, const uint8_t *b, hif4_f8_format b_fmt, int64_t N,
@@ -354,6 +356,8 @@ hif4_status hif4_layer_norm_f8(const void *x, hif4_dtype dtype, int64_t rows, in
  *            aligned, when dgamma or dbeta is wanted (the blocks' partial
  *            sums, joined in a fixed order); calls that overlap on the GPU
  *            need workspaces of their own.
+ * Rows of more than 8192 columns are taken at about half the rate of shorter
+ * ones (registers).
  * Errors: as hif4_layer_norm, and WORKSPACE.
  */
 size_t hif4_layer_norm_backward_workspace(int64_t rows, int64_t cols);
