@@ -61,7 +61,7 @@
 
 #include "hif4_f8.cuh"
 #include "hif4_pdl.cuh"
-#include "hif4_sm100.cuh"
+#include "hif4_sm100_f8.cuh"
 
 namespace hif4 {
 

@@ -43,9 +43,6 @@ uint64_t wait_limit_ns(uint64_t dflt);
 // Resident blocks per SM for `kernel` at this block size (cached per kernel
 // and device).
 int blocks_per_sm(const void *kernel, int threads, size_t dyn_smem);
-// Lets `kernel` use `bytes` of dynamic shared memory on the current device
-// (the attribute is set once per kernel, device and larger size).
-hif4_status allow_smem(const void *kernel, size_t bytes);
 // 2-D BF16 tensor map (inner x outer elements, rows row_stride_bytes apart)
 // with box_inner x box_outer boxes, optionally 128-byte swizzled; the driver's
 // encoder is resolved once through the runtime.  False if unavailable.

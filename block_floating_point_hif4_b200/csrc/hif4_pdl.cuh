@@ -17,6 +17,10 @@ __device__ __forceinline__ void pdl_enter()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device
+// (the attribute is set once per kernel, device and larger size).
+hif4_status allow_smem(const void *kernel, size_t bytes);
+
 template <typename... KArgs, typename... Args>
 hif4_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args)
 {
